@@ -34,6 +34,17 @@
  *   dmadesc_reg_register       batch of registrations (page-rounded, refcounted)
  *   dmadesc_reg_deregister     batch of deregistrations
  *
+ * and a paged 8-bit key/value cache, whose pages are what a serving process
+ * moves with the descriptors above (a page is a multiple of 512 bytes at
+ * pool + page * page bytes, so it is one request of dmadesc_build_prp):
+ *
+ *   dmadesc_kv_append          quantise new keys and values into the pages
+ *   dmadesc_kv_attend          attention of new tokens over the cached ones
+ *   dmadesc_kv_free / _fork / _reserve / _copy_pages / _compact
+ *                              end, branch and extend requests, copy shared
+ *                              pages, gather the live pages at the front
+ *   dmadesc_kv_check           which requests name bad pages or lengths
+ *
  * Sources (web pages, cited by title and section):
  *   [NCCL-26] "NCCL 专家课程 26：GPUDirect RDMA、DMA-BUF、MR 与注册缓存",
  *             sections "IB Backend MR Cache" and
@@ -121,7 +132,9 @@ enum dmadesc_op {
     DMADESC_OP_PARTITION = 3,
     DMADESC_OP_EMIT_SQE = 4,
     DMADESC_OP_REGISTRY = 5,
-    DMADESC_OP_BUILD_PUT = 6
+    DMADESC_OP_BUILD_PUT = 6,
+    DMADESC_OP_KV_RESERVE = 7,
+    DMADESC_OP_KV_COMPACT = 8
 };
 
 /* Largest nqueues dmadesc_partition_by_queue and dmadesc_emit_sqe accept. */
@@ -601,10 +614,171 @@ int dmadesc_reg_deregister(uint64_t *start, uint64_t *end, uint64_t *id, uint32_
                            const uint64_t *handle, uint64_t n, uint8_t *status,
                            void *ws, size_t ws_bytes, void *stream);
 
+/* A paged key/value cache held in 8 bits (host struct; the pointers are device
+ * memory). A page holds T = page_tokens tokens of H = kv_heads heads of
+ * D = dim values:
+ *   K codes   u8 [H][T][D]            (offset 0)
+ *   V codes   u8 [H][T/16][D][16]     (offset H T D; 16 tokens of a dimension lie together)
+ *   K scales  f32[H][T/16]            (offset 2 H T D)
+ *   V scales  f32[H][T/16]
+ * padded to a multiple of 512 bytes (dmadesc_kv_page_bytes). A value is its
+ * code times the scale of its block of 16 tokens and one head; scales are
+ * powers of two, 2^-64 or more. Page p lies at pool + p * page bytes. Token t
+ * of request r lies in page table[r * width + t / T].
+ *   pool         u8[npages][page bytes], 16-byte aligned
+ *   table        i32[rows][width] pages of each request; entries past the
+ *                length are not read
+ *   lens         i32[rows] tokens of each request, new ones included
+ *   page_tokens  a power of two, 16..1024; dim 64, 128 or 256;
+ *   codes        enum dmadesc_kv_codes
+ * Limits (-EINVAL past them): npages < 2^31, width * T < 2^31, rows < 2^24,
+ * kv_heads 1..1024, page bytes < 2^31. */
+enum dmadesc_kv_codes {
+    DMADESC_KV_E4M3 = 0,   /* 8-bit float, 4 exponent and 3 mantissa bits, largest 448 */
+    DMADESC_KV_INT8 = 1    /* two's complement; -127..127 are written               */
+};
+enum dmadesc_kv_type { DMADESC_KV_BF16 = 0, DMADESC_KV_FP16 = 1, DMADESC_KV_FP32 = 2 };
+typedef struct dmadesc_kv_cache {
+    void *pool;
+    const int32_t *table;
+    const int32_t *lens;
+    uint64_t npages;
+    uint32_t rows, width;
+    uint32_t kv_heads, page_tokens, dim, codes;
+} dmadesc_kv_cache;
+
+/* Per-request (or per-listed-row) outcome of the cache calls. */
+enum dmadesc_kv_status {
+    DMADESC_KV_OK = 0,
+    DMADESC_KV_EINVAL = 1,  /* row out of range, a length past the table, q_start out of order */
+    DMADESC_KV_EPAGE = 2,   /* the row names a page outside the pool                          */
+    DMADESC_KV_ENOSPC = 3   /* no free pages left for the row; nothing of it changed          */
+};
+
+/* Bytes of a page, 0 for sizes the cache does not take. Host-only. */
+size_t dmadesc_kv_page_bytes(uint32_t kv_heads, uint32_t page_tokens, uint32_t dim);
+
+/*
+ * dmadesc_kv_check - validation of a cache's table (the debug mode of
+ * dmadesc_kv_append and dmadesc_kv_attend, which give unspecified but
+ * memory-safe results for the requests it refuses: a bad page is neither read
+ * nor written).
+ *   q_start    i32[rows + 1] or NULL: as the call to be checked takes it
+ *   appending  nonzero: also refuse requests with more new tokens than length
+ *   status     u8[rows] enum dmadesc_kv_status
+ */
+int dmadesc_kv_check(const dmadesc_kv_cache *cache, const int32_t *q_start, uint64_t total,
+                     int appending, uint8_t *status, void *stream);
+
+/*
+ * dmadesc_kv_append - quantises new keys and values into the cache.
+ *
+ * Request r's new tokens are rows q_start[r] .. q_start[r+1]-1 of k and v, the
+ * last ones of its lens[r] tokens; its pages are in the table already
+ * (dmadesc_kv_reserve) and are written by no other request. Every touched
+ * block gets the least scale 2^e (e >= -64) under which all of its values fit
+ * the largest code, but no smaller scale than its earlier tokens had; codes
+ * are rounded once, ties to even, earlier tokens' again where the scale grew,
+ * and places of the block past the length become 0. An infinite value is
+ * stored as the largest code, a NaN as e4m3's NaN (0 in int8); neither counts
+ * for the scale.
+ *   k, v       [total][kv_heads][dim] of `type`, with strides in elements
+ *              between tokens and heads; dim contiguous. Base 16-byte aligned
+ *              and strides multiples of 8 (-EINVAL otherwise)
+ *   q_start    i32[rows + 1], q_start[0] = 0, non-decreasing, ends at total
+ *   total      new tokens of all requests, < 2^31
+ */
+int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_token_stride,
+                      int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                      int64_t v_head_stride, const int32_t *q_start, uint64_t total,
+                      uint32_t type, void *stream);
+
+/*
+ * dmadesc_kv_attend - attention of new tokens over the cached ones.
+ *
+ * For token j of request r (row q_start[r] + j of q) and head h, over the
+ * tokens t of the request's cache that it sees, with keys and values of head
+ * h / (heads / kv_heads):
+ *   s_t = scale * sum_d q_d K_td      o_d = sum_t softmax(s)_t V_td
+ *   lse = log sum_t exp(s_t)
+ * It sees t < lens[r]; with DMADESC_KV_CAUSAL only t <= lens[r] - n + j, n
+ * being the request's new tokens. A row that sees nothing gets o = 0 and
+ * lse = -inf. What lies past the length or is not seen never counts, whatever
+ * bits it holds. Scores, softmax and sums are f32; the probabilities are
+ * rounded to 11 bits for the product with V.
+ *   q          [total][heads][dim] of `type` (bf16 or fp16), strides in
+ *              elements; base 16-byte aligned, strides multiples of 8
+ *   heads      a multiple of kv_heads
+ *   scale      factor of the scores; 0 means 1 / sqrt(dim)
+ *   out        [total][heads][dim] of `type`, contiguous, 16-byte aligned
+ *   lse        f32[total][heads] or NULL
+ *   q_start, total   as dmadesc_kv_append (total * heads < 2^31)
+ * Workspace: dmadesc_kv_attend_workspace_bytes(...), for the partial results
+ * of requests whose cache is split over several workgroups.
+ */
+#define DMADESC_KV_CAUSAL 1u
+int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride,
+                      int64_t q_head_stride, const int32_t *q_start, uint64_t total,
+                      uint32_t heads, uint32_t type, uint32_t flags, float scale, void *out,
+                      float *lse, void *ws, size_t ws_bytes, void *stream);
+size_t dmadesc_kv_attend_workspace_bytes(uint64_t total, uint32_t rows, uint32_t heads,
+                                         uint32_t kv_heads, uint32_t dim, uint32_t width,
+                                         uint32_t page_tokens);
+
+/*
+ * Page operations. refs i32[npages] counts the rows that hold each page (0 =
+ * free); table and lens are as in dmadesc_kv_cache and are updated in place.
+ * A row of n tokens holds the pages of its first ceil(n / page_tokens) table
+ * entries. The listed rows of one call are distinct, and no row is both
+ * parent and child (otherwise the result is unspecified but memory-safe).
+ * status u8[n] (enum dmadesc_kv_status): a refused row is left as it was.
+ *
+ * dmadesc_kv_free: cuts row[i] to its first keep[i] tokens (keep NULL: none),
+ * dropping a reference of every page past them and setting all further table
+ * entries to -1. Cutting drafted tokens that were refused is its other use.
+ *
+ * dmadesc_kv_fork: child[i] (an empty row, lens 0) becomes a copy of
+ * parent[i], sharing its pages: each gains a reference.
+ *
+ * dmadesc_kv_reserve: extends slot[i] by n_new[i] tokens: free pages (refs 0 on
+ * entry) are handed out in ascending order to the slots in call order, one
+ * for each page the longer row needs and one in place of a partly filled last
+ * page that is shared (refs > 1 on entry): src[i] is then that page, dst[i] the
+ * one to copy it to, otherwise both are -1. A slot for which the pages run
+ * out, counting those of all slots before it, is refused with ENOSPC.
+ *   Workspace: dmadesc_workspace_bytes(DMADESC_OP_KV_RESERVE, npages, n).
+ *
+ * dmadesc_kv_compact: with L live pages (refs > 0), the live pages at or past L
+ * move, in ascending order, to the free pages below L, in ascending order;
+ * the table and refs are renamed. src, dst i32[npages / 2] list the moves,
+ * -1 past the last; *moves (device) counts them. The bytes are moved by
+ *
+ * dmadesc_kv_copy_pages: copies page src[i] to dst[i] for i < n (i < *count if
+ * count is given); an entry whose src or dst is outside the pool copies
+ * nothing. No dst is another entry's src or dst. page_bytes is a multiple of
+ * 16 and pool is 16-byte aligned.
+ */
+int dmadesc_kv_free(int32_t *refs, uint64_t npages, int32_t *table, int32_t *lens, uint32_t rows,
+                    uint32_t width, uint32_t page_tokens, const int32_t *row,
+                    const int32_t *keep, uint64_t n, uint8_t *status, void *stream);
+int dmadesc_kv_fork(int32_t *refs, uint64_t npages, int32_t *table, int32_t *lens, uint32_t rows,
+                    uint32_t width, uint32_t page_tokens, const int32_t *parent,
+                    const int32_t *child, uint64_t n, uint8_t *status, void *stream);
+int dmadesc_kv_reserve(int32_t *refs, uint64_t npages, int32_t *table, int32_t *lens,
+                       uint32_t rows, uint32_t width, uint32_t page_tokens, const int32_t *slot,
+                       const int32_t *n_new, uint64_t n, int32_t *src, int32_t *dst,
+                       uint8_t *status, void *ws, size_t ws_bytes, void *stream);
+int dmadesc_kv_compact(int32_t *refs, uint64_t npages, int32_t *table, uint32_t rows,
+                       uint32_t width, int32_t *src, int32_t *dst, int32_t *moves, void *ws,
+                       size_t ws_bytes, void *stream);
+int dmadesc_kv_copy_pages(void *pool, uint64_t npages, uint64_t page_bytes, const int32_t *src,
+                          const int32_t *dst, uint64_t n, const int32_t *count, void *stream);
+
 /* Workspace bytes needed by `op` for n requests (`param` = nqueues for
  * DMADESC_OP_PARTITION and DMADESC_OP_EMIT_SQE, the table capacity for
  * DMADESC_OP_REGISTRY, nregions for DMADESC_OP_MR_LOOKUP (its optional
- * record workspace), ignored otherwise). Returns 0 for an unknown op or
+ * record workspace), the listed rows for DMADESC_OP_KV_RESERVE (n is then the
+ * pages of the pool, as for DMADESC_OP_KV_COMPACT), ignored otherwise). Returns 0 for an unknown op or
  * for an op that needs none. Host-only; launches nothing. */
 size_t dmadesc_workspace_bytes(int op, uint64_t n, uint32_t param);
 

@@ -23,12 +23,19 @@ __all__ = ["mr_lookup", "build_prp", "build_prp_packed", "build_prp_packed_noall
            "SQ_MAX_DEPTH",
            "mr_table_check", "debug_wait_limit", "DEFAULT_WAIT_POLLS",
            "MISS", "EXACT", "CONTAINED", "INVALID",
-           "PRP_OK", "PRP_EINVAL", "PRP_ERANGE", "PRP_ENOSPC", "PRP_EBUSY"]
+           "PRP_OK", "PRP_EINVAL", "PRP_ERANGE", "PRP_ENOSPC", "PRP_EBUSY",
+           "kv_page_bytes", "kv_append", "kv_attend", "kv_check", "kv_free", "kv_fork",
+           "kv_reserve", "kv_compact", "kv_copy_pages",
+           "KV_E4M3", "KV_INT8", "KV_OK", "KV_EINVAL", "KV_EPAGE", "KV_ENOSPC"]
 
 LIB_PATH = _build.LIB
 MAX_QUEUES = 256
 SQ_MAX_DEPTH = 65536
 OP_MR_LOOKUP, OP_BUILD_PRP, OP_PARTITION, OP_EMIT_SQE, OP_REGISTRY, OP_BUILD_PUT = 1, 2, 3, 4, 5, 6
+OP_KV_RESERVE, OP_KV_COMPACT = 7, 8
+KV_E4M3, KV_INT8 = 0, 1
+KV_OK, KV_EINVAL, KV_EPAGE, KV_ENOSPC = 0, 1, 2, 3
+KV_CAUSAL = 1
 REG_MAX_BATCH, REG_MAX_CAPACITY = 65536, 1 << 24
 REG_INVALID, REG_HIT, REG_NEW, REG_HIT_NEW, REG_NOSPACE = 0, 1, 2, 3, 4
 DEREG_OK, DEREG_REMOVED, DEREG_STALE = 0, 1, 2
@@ -40,6 +47,15 @@ _P = ctypes.c_void_p
 _U64 = ctypes.c_uint64
 _U32 = ctypes.c_uint32
 _SIZE = ctypes.c_size_t
+_I64 = ctypes.c_int64
+
+
+class _KvCache(ctypes.Structure):
+    """dmadesc_kv_cache"""
+    _fields_ = [("pool", _P), ("table", _P), ("lens", _P), ("npages", _U64), ("rows", _U32),
+                ("width", _U32), ("kv_heads", _U32), ("page_tokens", _U32), ("dim", _U32),
+                ("codes", _U32)]
+
 
 _EXPORTS = {
     "dmadesc_mr_lookup": ([_P, _P, _P, _U32, _U32, _P, _P, _U64, _U64,
@@ -65,6 +81,18 @@ _EXPORTS = {
     "dmadesc_build_batch": ([_P, _P, _P, _U32, _U32, _U64, _P, _U64, _P, _P, _P, _U64, _U32,
                              _U64, _P, _U64, _U32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                              _P, _P, _SIZE, _P], ctypes.c_int),
+    "dmadesc_kv_page_bytes": ([_U32, _U32, _U32], _SIZE),
+    "dmadesc_kv_check": ([_P, _P, _U64, ctypes.c_int, _P, _P], ctypes.c_int),
+    "dmadesc_kv_append": ([_P, _P, _I64, _I64, _P, _I64, _I64, _P, _U64, _U32, _P], ctypes.c_int),
+    "dmadesc_kv_attend": ([_P, _P, _I64, _I64, _P, _U64, _U32, _U32, _U32, ctypes.c_float,
+                           _P, _P, _P, _SIZE, _P], ctypes.c_int),
+    "dmadesc_kv_attend_workspace_bytes": ([_U64, _U32, _U32, _U32, _U32, _U32, _U32], _SIZE),
+    "dmadesc_kv_free": ([_P, _U64, _P, _P, _U32, _U32, _U32, _P, _P, _U64, _P, _P], ctypes.c_int),
+    "dmadesc_kv_fork": ([_P, _U64, _P, _P, _U32, _U32, _U32, _P, _P, _U64, _P, _P], ctypes.c_int),
+    "dmadesc_kv_reserve": ([_P, _U64, _P, _P, _U32, _U32, _U32, _P, _P, _U64, _P, _P, _P, _P,
+                            _SIZE, _P], ctypes.c_int),
+    "dmadesc_kv_compact": ([_P, _U64, _P, _U32, _U32, _P, _P, _P, _P, _SIZE, _P], ctypes.c_int),
+    "dmadesc_kv_copy_pages": ([_P, _U64, _U64, _P, _P, _U64, _P, _P], ctypes.c_int),
     "dmadesc_batch_workspace_bytes": ([_U64, _U32, _U32], _SIZE),
     "dmadesc_workspace_bytes": ([ctypes.c_int, _U64, _U32], _SIZE),
     "dmadesc_strerror": ([ctypes.c_int], ctypes.c_char_p),
@@ -609,3 +637,231 @@ class DeviceRegistry:
         order = host["by_start"].astype(np.int64)
         return ((host["start"][order], host["end"][order], host["id"][order],
                  host["refs"][order].astype(np.int64)), host["id"])
+
+
+# -------------------------------------------------- paged 8-bit key/value cache ---
+
+_KV_TYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def kv_page_bytes(kv_heads: int, page_tokens: int, dim: int) -> int:
+    """Bytes of a page of the cache (a multiple of 512); 0 for sizes it does not take."""
+    return int(lib().dmadesc_kv_page_bytes(kv_heads, page_tokens, dim))
+
+
+def _kv_new(size, dtype, device, stream):
+    """A device tensor the call fills on `stream` (which may not be the
+    current one: the allocator must not hand the memory out before it is done)."""
+    t = torch.empty(size, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes):
+    if table.dim() != 2 or pool.dim() != 2:
+        raise ValueError("pool must be u8[npages, page_bytes] and table i32[rows, width]")
+    rows, width = table.shape
+    npages, nbytes = pool.shape
+    need = kv_page_bytes(kv_heads, page_tokens, dim)
+    if need == 0 or nbytes != need:
+        raise ValueError(f"a page of {kv_heads} heads x {page_tokens} tokens x {dim} values "
+                         f"takes {need or 'no'} bytes, pool has {nbytes}")
+    return _KvCache(_dev(pool, torch.uint8, "pool"), _dev(table, torch.int32, "table"),
+                    _dev(lens, torch.int32, "lens", rows), npages, rows, width, kv_heads,
+                    page_tokens, dim, codes)
+
+
+def _kv_rows(t, name, total, heads, dim, types):
+    """(pointer, token stride, head stride) of a [total, heads, dim] operand."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a device tensor, got {t.device}")
+    if t.dtype not in types:
+        raise TypeError(f"{name}: {t.dtype} is not taken")
+    if t.shape != (total, heads, dim):
+        raise ValueError(f"{name}: expected shape {(total, heads, dim)}, got {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _kv_refused(func: str, status: torch.Tensor, stream, out: dict) -> None:
+    """Synchronizes and raises DmadescRefused if some row was refused."""
+    if stream is not None:
+        stream.synchronize()
+    bad = int((status != KV_OK).sum().item()) if status.numel() else 0
+    if bad:
+        raise DmadescRefused(f"{func}: {bad} row(s) refused (status: 1 bad row, length or "
+                             "q_start, 2 bad page, 3 no free pages)", out)
+
+
+def kv_check(q_start: torch.Tensor | None, total: int, pool: torch.Tensor, table: torch.Tensor,
+             lens: torch.Tensor, kv_heads: int, page_tokens: int, dim: int,
+             appending: bool = False, stream=None) -> torch.Tensor:
+    """Status u8[rows] (KV_OK, KV_EINVAL, KV_EPAGE) of a cache's table, lengths
+    and, unless None, q_start (dmadesc_kv_check)."""
+    cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, 0)
+    status = _kv_new(table.shape[0], torch.uint8, pool.device, stream)
+    q = None if q_start is None else _dev(q_start, torch.int32, "q_start", table.shape[0] + 1)
+    rc = lib().dmadesc_kv_check(ctypes.byref(cache), q, total, appending, status.data_ptr(),
+                                _stream(pool.device, stream))
+    _check("dmadesc_kv_check", rc)
+    return status
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor,
+              table: torch.Tensor, lens: torch.Tensor, page_tokens: int, codes: int = KV_E4M3,
+              stream=None, check: bool = True) -> None:
+    """Quantises new keys and values [total, kv_heads, dim] (bf16, fp16 or f32,
+    strided views included) into the cache's pages; `lens` counts them already.
+    check=True first checks the table (kv_check), synchronizes and raises
+    DmadescRefused if a request names a bad page or length."""
+    total, heads, dim = k.shape
+    cache = _kv_cache(pool, table, lens, heads, page_tokens, dim, codes)
+    kp = _kv_rows(k, "k", total, heads, dim, _KV_TYPE)
+    vp = _kv_rows(v, "v", total, heads, dim, (k.dtype,))
+    q = _dev(q_start, torch.int32, "q_start", table.shape[0] + 1)
+    if check:
+        status = kv_check(q_start, total, pool, table, lens, heads, page_tokens, dim, True, stream)
+        _kv_refused("dmadesc_kv_append", status, stream, dict(status=status))
+    rc = lib().dmadesc_kv_append(ctypes.byref(cache), *kp, *vp, q, total, _KV_TYPE[k.dtype],
+                                 _stream(pool.device, stream))
+    _check("dmadesc_kv_append", rc)
+
+
+def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table: torch.Tensor,
+              lens: torch.Tensor, kv_heads: int, page_tokens: int, codes: int = KV_E4M3,
+              causal: bool = True, scale: float | None = None, out: dict | None = None,
+              ws: torch.Tensor | None = None, stream=None, check: bool = True) -> dict:
+    """Attention of q [total, heads, dim] (bf16 or fp16) over the cache; returns
+    dict(out, lse): out as q, lse f32[total, heads]. scale None means
+    1 / sqrt(dim). check=True first checks the table (kv_check), synchronizes
+    and raises DmadescRefused if a request names a bad page or length."""
+    total, heads, dim = q.shape
+    dev = q.device
+    cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes)
+    qp = _kv_rows(q, "q", total, heads, dim, (torch.bfloat16, torch.float16))
+    qs = _dev(q_start, torch.int32, "q_start", cache.rows + 1)
+    if check:
+        status = kv_check(q_start, total, pool, table, lens, kv_heads, page_tokens, dim, False,
+                          stream)
+        _kv_refused("dmadesc_kv_attend", status, stream, dict(status=status))
+    if out is None:
+        out = dict(out=_kv_new((total, heads, dim), q.dtype, dev, stream),
+                   lse=_kv_new((total, heads), torch.float32, dev, stream))
+    need = lib().dmadesc_kv_attend_workspace_bytes(total, cache.rows, heads, kv_heads, dim,
+                                                   cache.width, page_tokens)
+    if ws is None:
+        ws = _kv_new(need, torch.uint8, dev, stream)
+    rc = lib().dmadesc_kv_attend(
+        ctypes.byref(cache), *qp, qs, total, heads, _KV_TYPE[q.dtype],
+        KV_CAUSAL if causal else 0, 0.0 if scale is None else scale,
+        _dev(out["out"], q.dtype, "out", total * heads * dim),
+        _dev(out["lse"], torch.float32, "lse", total * heads), _dev(ws, torch.uint8, "ws"),
+        ws.numel(), _stream(dev, stream))
+    _check("dmadesc_kv_attend", rc)
+    return out
+
+
+def _kv_state(refs, table, lens, page_tokens):
+    if table.dim() != 2:
+        raise ValueError("table must be i32[rows, width]")
+    rows, width = table.shape
+    return (_dev(refs, torch.int32, "refs"), refs.numel(), _dev(table, torch.int32, "table"),
+            _dev(lens, torch.int32, "lens", rows), rows, width, page_tokens)
+
+
+def kv_free(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, row: torch.Tensor,
+            page_tokens: int, keep: torch.Tensor | None = None, stream=None,
+            check: bool = True) -> dict:
+    """Cuts the listed rows to their first keep[i] tokens (None: ends them) and
+    drops their references of the pages past them; returns dict(status).
+    check=True synchronizes and raises DmadescRefused for refused rows."""
+    n = row.numel()
+    status = _kv_new(n, torch.uint8, refs.device, stream)
+    k = None if keep is None else _dev(keep, torch.int32, "keep", n)
+    rc = lib().dmadesc_kv_free(*_kv_state(refs, table, lens, page_tokens),
+                               _dev(row, torch.int32, "row"), k, n, status.data_ptr(),
+                               _stream(refs.device, stream))
+    _check("dmadesc_kv_free", rc)
+    out = dict(status=status)
+    if check:
+        _kv_refused("dmadesc_kv_free", status, stream, out)
+    return out
+
+
+def kv_fork(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, parent: torch.Tensor,
+            child: torch.Tensor, page_tokens: int, stream=None, check: bool = True) -> dict:
+    """Makes each empty row child[i] a copy of row parent[i] that shares its
+    pages; returns dict(status). check=True synchronizes and raises
+    DmadescRefused for refused rows."""
+    n = parent.numel()
+    status = _kv_new(n, torch.uint8, refs.device, stream)
+    rc = lib().dmadesc_kv_fork(*_kv_state(refs, table, lens, page_tokens),
+                               _dev(parent, torch.int32, "parent"),
+                               _dev(child, torch.int32, "child", n), n, status.data_ptr(),
+                               _stream(refs.device, stream))
+    _check("dmadesc_kv_fork", rc)
+    out = dict(status=status)
+    if check:
+        _kv_refused("dmadesc_kv_fork", status, stream, out)
+    return out
+
+
+def kv_reserve(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, slot: torch.Tensor,
+               n_new: torch.Tensor, page_tokens: int, ws: torch.Tensor | None = None, stream=None,
+               check: bool = True) -> dict:
+    """Extends rows slot[i] by n_new[i] tokens with free pages; returns dict(src,
+    dst, status): pages to copy with kv_copy_pages, -1 where there is none.
+    check=True synchronizes and raises DmadescRefused for refused rows (KV_ENOSPC:
+    the free pages ran out)."""
+    n = slot.numel()
+    dev = refs.device
+    out = dict(src=_kv_new(n, torch.int32, dev, stream), dst=_kv_new(n, torch.int32, dev, stream),
+               status=_kv_new(n, torch.uint8, dev, stream))
+    if ws is None:
+        ws = _kv_new(workspace_bytes(OP_KV_RESERVE, refs.numel(), n), torch.uint8, dev, stream)
+    rc = lib().dmadesc_kv_reserve(
+        *_kv_state(refs, table, lens, page_tokens), _dev(slot, torch.int32, "slot"),
+        _dev(n_new, torch.int32, "n_new", n), n, out["src"].data_ptr(), out["dst"].data_ptr(),
+        out["status"].data_ptr(), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(dev, stream))
+    _check("dmadesc_kv_reserve", rc)
+    if check:
+        _kv_refused("dmadesc_kv_reserve", out["status"], stream, out)
+    return out
+
+
+def kv_compact(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, page_tokens: int,
+               ws: torch.Tensor | None = None, stream=None) -> dict:
+    """Renames the live pages so that they are the first ones; returns dict(src,
+    dst, moves): the pages to copy with kv_copy_pages(count=moves), -1 past the
+    last. Takes the state as the other page calls do; lens does not change."""
+    state = _kv_state(refs, table, lens, page_tokens)
+    npages = refs.numel()
+    dev = refs.device
+    out = dict(src=_kv_new(npages // 2, torch.int32, dev, stream),
+               dst=_kv_new(npages // 2, torch.int32, dev, stream),
+               moves=_kv_new(1, torch.int32, dev, stream))
+    if ws is None:
+        ws = _kv_new(workspace_bytes(OP_KV_COMPACT, npages), torch.uint8, dev, stream)
+    rc = lib().dmadesc_kv_compact(state[0], npages, state[2], state[4], state[5],
+                                  out["src"].data_ptr(), out["dst"].data_ptr(),
+                                  out["moves"].data_ptr(), _dev(ws, torch.uint8, "ws"),
+                                  ws.numel(), _stream(dev, stream))
+    _check("dmadesc_kv_compact", rc)
+    return out
+
+
+def kv_copy_pages(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+                  count: torch.Tensor | None = None, stream=None) -> None:
+    """Copies page src[i] to dst[i] of `pool` (u8[npages, page_bytes]); entries
+    outside the pool (-1) copy nothing. count: device i32[1], entries to look at."""
+    if pool.dim() != 2:
+        raise ValueError("pool must be u8[npages, page_bytes]")
+    n = src.numel()
+    c = None if count is None else _dev(count, torch.int32, "count", 1)
+    rc = lib().dmadesc_kv_copy_pages(_dev(pool, torch.uint8, "pool"), pool.shape[0], pool.shape[1],
+                                     _dev(src, torch.int32, "src"),
+                                     _dev(dst, torch.int32, "dst", n), n, c,
+                                     _stream(pool.device, stream))
+    _check("dmadesc_kv_copy_pages", rc)

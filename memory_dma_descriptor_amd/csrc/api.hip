@@ -74,6 +74,46 @@ int build_prp_common(const uint64_t *lut, uint64_t lut_entries, const uint64_t *
     return launched(dd::launch_build_prp(a, static_cast<hipStream_t>(stream)));
 }
 
+constexpr uint64_t kMaxPages = 1ull << 31;       // page ids are i32
+
+bool kv_sizes_ok(uint32_t kv_heads, uint32_t page_tokens, uint32_t dim)
+{
+    if (kv_heads < 1 || kv_heads > 1024) return false;
+    if (page_tokens < 16 || page_tokens > 1024 || (page_tokens & (page_tokens - 1))) return false;
+    if (dim != 64 && dim != 128 && dim != 256) return false;
+    return dd::kv_page_bytes(kv_heads, page_tokens, dim) < (1ull << 31);
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool kv_cache_ok(const dmadesc_kv_cache *c)
+{
+    if (!c || !kv_sizes_ok(c->kv_heads, c->page_tokens, c->dim)) return false;
+    if (c->codes > DMADESC_KV_INT8 || c->npages >= kMaxPages || c->rows >= (1u << 24)) return false;
+    if ((uint64_t)c->width * c->page_tokens >= (1ull << 31)) return false;
+    if (c->npages > 0 && (!c->pool || !aligned16(c->pool))) return false;
+    if (c->rows > 0 && (!c->lens || !aligned4(c->lens))) return false;
+    if ((uint64_t)c->rows * c->width > 0 && (!c->table || !aligned4(c->table))) return false;
+    return true;
+}
+
+// A [total][heads][dim] operand: 16-byte loads of its rows.
+bool kv_rows_ok(const void *p, int64_t tok, int64_t head)
+{
+    return p && aligned16(p) && tok >= 0 && head >= 0 && (tok & 7) == 0 && (head & 7) == 0;
+}
+
+bool kv_pages_ok(const int32_t *refs, uint64_t npages, const int32_t *table, uint32_t rows,
+                 uint32_t width, uint32_t page_tokens)
+{
+    if (npages >= kMaxPages || rows >= (1u << 24)) return false;
+    if (page_tokens < 16 || page_tokens > 1024 || (page_tokens & (page_tokens - 1))) return false;
+    if ((uint64_t)width * page_tokens >= (1ull << 31)) return false;
+    if (npages > 0 && !refs) return false;
+    return (uint64_t)rows * width == 0 || table;
+}
+
 }  // namespace
 
 namespace dd {
@@ -112,6 +152,8 @@ size_t dmadesc_workspace_bytes(int op, uint64_t n, uint32_t param)
         if (param == 0 || param > DMADESC_MAX_QUEUES) return 0;
         return dd::ws_emit_sqe(param);
     case DMADESC_OP_BUILD_PUT: return dd::ws_build_put(n);
+    case DMADESC_OP_KV_RESERVE: return n < kMaxPages ? dd::ws_kv_reserve(n, param) : 0;
+    case DMADESC_OP_KV_COMPACT: return n < kMaxPages ? dd::ws_kv_compact(n) : 0;
     case DMADESC_OP_REGISTRY:
         if (n > DMADESC_REG_MAX_BATCH || param > DMADESC_REG_MAX_CAPACITY) return 0;
         return dd::ws_registry(n, param);
@@ -339,6 +381,132 @@ int dmadesc_reg_deregister(uint64_t *start, uint64_t *end, uint64_t *id, uint32_
     dd::RegArgs a{start, end, id, refs, by_start, state, capacity, 12, nullptr, nullptr,
                   handle, n, nullptr, nullptr, nullptr, status, ws};
     return launched(dd::launch_reg_deregister(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t dmadesc_kv_page_bytes(uint32_t kv_heads, uint32_t page_tokens, uint32_t dim)
+{
+    return kv_sizes_ok(kv_heads, page_tokens, dim) ? dd::kv_page_bytes(kv_heads, page_tokens, dim)
+                                                   : 0;
+}
+
+int dmadesc_kv_check(const dmadesc_kv_cache *cache, const int32_t *q_start, uint64_t total,
+                     int appending, uint8_t *status, void *stream)
+{
+    if (!kv_cache_ok(cache) || total >= (1ull << 31)) return -EINVAL;
+    if (cache->rows == 0) return 0;
+    if (!status) return -EINVAL;
+    return launched(dd::launch_kv_check(*cache, q_start, total, appending != 0, status,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_token_stride,
+                      int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                      int64_t v_head_stride, const int32_t *q_start, uint64_t total,
+                      uint32_t type, void *stream)
+{
+    if (!kv_cache_ok(cache) || total >= (1ull << 31) || type > DMADESC_KV_FP32) return -EINVAL;
+    if (total == 0 || cache->rows == 0) return 0;
+    if (!q_start || !kv_rows_ok(k, k_token_stride, k_head_stride) ||
+        !kv_rows_ok(v, v_token_stride, v_head_stride))
+        return -EINVAL;
+    if (cache->npages == 0 || cache->width == 0) return 0;        // no page to write
+    dd::KvAppendArgs a{*cache, k, v, k_token_stride, k_head_stride, v_token_stride,
+                       v_head_stride, q_start, total, type};
+    return launched(dd::launch_kv_append(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t dmadesc_kv_attend_workspace_bytes(uint64_t total, uint32_t rows, uint32_t heads,
+                                         uint32_t kv_heads, uint32_t dim, uint32_t width,
+                                         uint32_t page_tokens)
+{
+    if (!kv_sizes_ok(kv_heads, page_tokens, dim) || heads == 0 || heads % kv_heads) return 0;
+    if (total == 0 || total >= (1ull << 31) || total * heads >= (1ull << 31) || rows == 0 ||
+        rows >= (1u << 24) || (uint64_t)width * page_tokens >= (1ull << 31))
+        return 0;
+    return dd::ws_kv_attend(total, rows, heads, kv_heads, dim, (uint64_t)width * page_tokens);
+}
+
+int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride,
+                      int64_t q_head_stride, const int32_t *q_start, uint64_t total,
+                      uint32_t heads, uint32_t type, uint32_t flags, float scale, void *out,
+                      float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!kv_cache_ok(cache) || total >= (1ull << 31) || (flags & ~DMADESC_KV_CAUSAL)) return -EINVAL;
+    if (type > DMADESC_KV_FP16 || heads == 0 || heads % cache->kv_heads) return -EINVAL;
+    if (total * heads >= (1ull << 31) || !(scale == scale)) return -EINVAL;
+    if (total == 0 || cache->rows == 0) return 0;
+    if (!q_start || !kv_rows_ok(q, q_token_stride, q_head_stride)) return -EINVAL;
+    if (!out || !aligned16(out) || !aligned4(lse)) return -EINVAL;
+    const uint64_t tokens = (uint64_t)cache->width * cache->page_tokens;
+    const size_t need = dd::ws_kv_attend(total, cache->rows, heads, cache->kv_heads, cache->dim,
+                                         tokens);
+    if (need > 0 && !ws_ok(ws, ws_bytes, need)) return -EINVAL;
+    dd::KvAttendArgs a{*cache, q, q_token_stride, q_head_stride, q_start, total, heads, type,
+                       (flags & DMADESC_KV_CAUSAL) != 0, scale, out, lse, ws};
+    return launched(dd::launch_kv_attend(a, static_cast<hipStream_t>(stream)));
+}
+
+int dmadesc_kv_free(int32_t *refs, uint64_t npages, int32_t *table, int32_t *lens, uint32_t rows,
+                    uint32_t width, uint32_t page_tokens, const int32_t *row,
+                    const int32_t *keep, uint64_t n, uint8_t *status, void *stream)
+{
+    if (!kv_pages_ok(refs, npages, table, rows, width, page_tokens) || n >= (1u << 24))
+        return -EINVAL;
+    if (n == 0) return 0;
+    if (!row || !status || (rows > 0 && !lens)) return -EINVAL;
+    dd::KvPageArgs k{refs, npages, table, lens, rows, width, page_tokens, (uint32_t)n, status};
+    return launched(dd::launch_kv_free(k, row, keep, static_cast<hipStream_t>(stream)));
+}
+
+int dmadesc_kv_fork(int32_t *refs, uint64_t npages, int32_t *table, int32_t *lens, uint32_t rows,
+                    uint32_t width, uint32_t page_tokens, const int32_t *parent,
+                    const int32_t *child, uint64_t n, uint8_t *status, void *stream)
+{
+    if (!kv_pages_ok(refs, npages, table, rows, width, page_tokens) || n >= (1u << 24))
+        return -EINVAL;
+    if (n == 0) return 0;
+    if (!parent || !child || !status || (rows > 0 && !lens)) return -EINVAL;
+    dd::KvPageArgs k{refs, npages, table, lens, rows, width, page_tokens, (uint32_t)n, status};
+    return launched(dd::launch_kv_fork(k, parent, child, static_cast<hipStream_t>(stream)));
+}
+
+int dmadesc_kv_reserve(int32_t *refs, uint64_t npages, int32_t *table, int32_t *lens,
+                       uint32_t rows, uint32_t width, uint32_t page_tokens, const int32_t *slot,
+                       const int32_t *n_new, uint64_t n, int32_t *src, int32_t *dst,
+                       uint8_t *status, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!kv_pages_ok(refs, npages, table, rows, width, page_tokens) || n >= (1u << 24))
+        return -EINVAL;
+    if (n == 0) return 0;
+    if (!slot || !n_new || !src || !dst || !status || (rows > 0 && !lens)) return -EINVAL;
+    if (!ws_ok(ws, ws_bytes, dd::ws_kv_reserve(npages, n))) return -EINVAL;
+    dd::KvPageArgs k{refs, npages, table, lens, rows, width, page_tokens, (uint32_t)n, status};
+    return launched(dd::launch_kv_reserve(k, slot, n_new, src, dst, ws,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+int dmadesc_kv_compact(int32_t *refs, uint64_t npages, int32_t *table, uint32_t rows,
+                       uint32_t width, int32_t *src, int32_t *dst, int32_t *moves, void *ws,
+                       size_t ws_bytes, void *stream)
+{
+    if (!kv_pages_ok(refs, npages, table, rows, width, 16)) return -EINVAL;
+    if (!moves || (npages >= 2 && (!src || !dst))) return -EINVAL;
+    if (!ws_ok(ws, ws_bytes, dd::ws_kv_compact(npages))) return -EINVAL;
+    dd::KvPageArgs k{refs, npages, table, nullptr, rows, width, 16, 0, nullptr};
+    return launched(dd::launch_kv_compact(k, src, dst, moves, ws,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+int dmadesc_kv_copy_pages(void *pool, uint64_t npages, uint64_t page_bytes, const int32_t *src,
+                          const int32_t *dst, uint64_t n, const int32_t *count, void *stream)
+{
+    if (npages >= kMaxPages || page_bytes == 0 || (page_bytes & 15) || page_bytes >= (1ull << 31))
+        return -EINVAL;
+    if (n >= kMaxPages) return -EINVAL;
+    if (n == 0 || npages == 0) return 0;
+    if (!pool || !aligned16(pool) || !src || !dst) return -EINVAL;
+    return launched(dd::launch_kv_copy(pool, npages, page_bytes, src, dst, n, count,
+                                       static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -95,6 +95,40 @@ struct PutArgs {
     void *ws;
 };
 
+struct KvView;
+
+struct KvAppendArgs {
+    dmadesc_kv_cache cache;
+    const void *k, *v;
+    int64_t k_tok, k_head, v_tok, v_head;   // strides in elements
+    const int32_t *q_start;
+    uint64_t total;
+    uint32_t type;
+};
+
+struct KvAttendArgs {
+    dmadesc_kv_cache cache;
+    const void *q;
+    int64_t q_tok, q_head;                  // strides in elements
+    const int32_t *q_start;
+    uint64_t total;
+    uint32_t heads, type;
+    bool causal;
+    float scale;
+    void *out;
+    float *lse;                             // or nullptr
+    void *ws;
+};
+
+struct KvPageArgs {
+    int32_t *refs;
+    uint64_t npages;
+    int32_t *table, *lens;
+    uint32_t rows, width, page_tokens;
+    uint32_t n;                             // listed rows
+    uint8_t *status;
+};
+
 hipError_t launch_mr_lookup(const LookupArgs &a, hipStream_t s);
 hipError_t launch_table_check(const uint64_t *rs, const uint64_t *re, uint32_t nregions,
                               uint32_t page_shift, uint64_t *scratch, uint64_t *host_result,
@@ -122,6 +156,31 @@ hipError_t launch_build_put(const PutArgs &a, hipStream_t s);
 hipError_t launch_reg_register(const RegArgs &a, hipStream_t s);
 hipError_t launch_reg_deregister(const RegArgs &a, hipStream_t s);
 
+// Bytes of a page: codes and scales of K and V, padded to a logical block.
+inline uint64_t kv_page_bytes(uint64_t heads, uint64_t tokens, uint64_t dim)
+{
+    return (2 * heads * tokens * dim + 8 * heads * (tokens / 16) + 511) & ~511ull;
+}
+KvView kv_view(const dmadesc_kv_cache &c);
+hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s);
+hipError_t launch_kv_attend(const KvAttendArgs &a, hipStream_t s);
+hipError_t launch_kv_check(const dmadesc_kv_cache &c, const int32_t *q_start, uint64_t total,
+                           bool appending, uint8_t *status, hipStream_t s);
+hipError_t launch_kv_free(const KvPageArgs &k, const int32_t *row, const int32_t *keep,
+                          hipStream_t s);
+hipError_t launch_kv_fork(const KvPageArgs &k, const int32_t *parent, const int32_t *child,
+                          hipStream_t s);
+hipError_t launch_kv_reserve(const KvPageArgs &k, const int32_t *slot, const int32_t *n_new,
+                             int32_t *src, int32_t *dst, void *ws, hipStream_t s);
+hipError_t launch_kv_compact(const KvPageArgs &k, int32_t *src, int32_t *dst, int32_t *moves,
+                             void *ws, hipStream_t s);
+hipError_t launch_kv_copy(void *pool, uint64_t npages, uint64_t page_bytes, const int32_t *src,
+                          const int32_t *dst, uint64_t n, const int32_t *count, hipStream_t s);
+
+size_t ws_kv_attend(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads,
+                    uint32_t dim, uint64_t tokens);
+size_t ws_kv_reserve(uint64_t npages, uint64_t n);
+size_t ws_kv_compact(uint64_t npages);
 size_t ws_mr_lookup(uint32_t nregions);
 size_t ws_build_prp(uint64_t n);
 size_t ws_partition(uint64_t n, uint32_t nqueues);
