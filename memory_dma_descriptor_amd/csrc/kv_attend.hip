@@ -31,9 +31,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 64;                   // tokens a wave handles at a time
-constexpr uint32_t kTarget = 1024;          // workgroups that a call is split into
-constexpr uint32_t kMinTiles = 16;          // least tiles of a split
+// Workgroups that a call's work is cut into, and the least tiles of a part:
+// for the kernel of few rows and for that of many.
+constexpr uint32_t kTargetFew = 1024, kMinTilesFew = 16;
+constexpr uint32_t kTargetMany = 512, kMinTilesMany = 4;
 constexpr uint32_t kMaxSplits = 256;
+constexpr uint32_t kRowsMany = 128;         // query rows of a workgroup of the kernel of many
+constexpr uint32_t kMostFew = 64;           // query rows per key head up to which rows are few
 constexpr float kShift = 15.0f;             // probabilities are at most 2^15 in f16
 
 struct AttendArgs {
@@ -50,12 +54,13 @@ struct AttendArgs {
     float *part_lse;                        // [slots][rows of a tile], base 2
     uint2 *plan;                            // [rows] first slot and splits of each request
     uint32_t slots;
+    uint32_t least, most;                   // requests of least..most query rows are this kernel's
 };
 
-// One piece of work: `count` tiles of the cache from `first`, for one row
-// tile of one key head of request b.
+// One piece of work: the split-th of `splits` even parts of the cache that one
+// row tile of one key head of request b sees.
 struct Item {
-    uint32_t b, split, splits, head, rt, base, first, count;
+    uint32_t b, split, splits, head, rt, base;
 };
 
 template <int kQ> struct QFrag;
@@ -111,14 +116,16 @@ __device__ __forceinline__ V8 codes8(uint32_t lo, uint32_t hi)
     return V8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Row tiles and cache tiles of request b.
+// Row tiles and cache tiles of request b; no row tiles if it is not this
+// kernel's.
 template <int kRows>
 __device__ __forceinline__ void request_size(const AttendArgs &a, uint32_t b, uint32_t &rts,
                                              uint32_t &tiles)
 {
     uint32_t s0, s1;
     kv_span(a.q_start, b, a.total, s0, s1);
-    rts = (uint32_t)(((uint64_t)(s1 - s0) * a.group + kRows - 1) / kRows);
+    const uint32_t n = (s1 - s0) * a.group;             // total * heads < 2^31
+    rts = n < a.least || n > a.most ? 0u : (n + kRows - 1) / kRows;
     tiles = ((uint32_t)kv_len(a.c, b) + kTile - 1) / kTile;
 }
 
@@ -133,7 +140,7 @@ __device__ __forceinline__ uint32_t splits_of(uint32_t tiles, uint32_t chunk)
 // kTarget pieces of equal size. Every workgroup adds the lengths up for
 // itself, one round for up to 256 requests, which costs less than a launch
 // that would do it once. Returns false for workgroups past the last item.
-template <int kRows>
+template <int kRows, uint32_t kTarget, uint32_t kMinTiles>
 __device__ bool find_item(const AttendArgs &a, uint32_t id, Item &it)
 {
     __shared__ uint64_t sums[kWaves];
@@ -170,16 +177,12 @@ __device__ bool find_item(const AttendArgs &a, uint32_t id, Item &it)
         const uint64_t at = run + block_excl_scan<kThreads, uint32_t>(mine, scan, &all);
         if (id >= at && id < at + mine) {
             const uint32_t k = id - (uint32_t)at;
-            const uint32_t per = (tiles + splits - 1) / splits;
             found.b = b;
-            found.rt = k % rts;
-            found.head = k / rts % heads;
-            found.split = k / rts / heads;
+            found.head = k % heads;        // workgroups go round the 8 XCDs: a head's on few of them
+            found.rt = k / heads % rts;
+            found.split = k / heads / rts;
             found.splits = splits;
             found.base = (uint32_t)at;
-            found.first = found.split * per;
-            found.count = found.first >= tiles ? 0u
-                          : (tiles - found.first < per ? tiles - found.first : per);
             hit = 1;
         }
         __syncthreads();
@@ -212,6 +215,30 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// w without the bytes that nan_bytes found.
+__device__ __forceinline__ uint32_t without(uint32_t w, uint32_t nans)
+{
+    return w & ~(nans | (nans - (nans >> 7)));
+}
+
+// The first `keep` bytes of word q of a run of 16.
+__device__ __forceinline__ uint32_t keep_mask(int keep, int q)
+{
+    const int n = keep - 4 * q;
+    return n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+}
+
+// A NaN code of V must reach the rows that see its token and no other, but in
+// a product 0 * NaN is NaN. In the tiles that some row sees only in part it is
+// therefore replaced by 0 and its token noted per dimension, the first one:
+// rows see the tokens up to their limit, so a row whose limit reaches that
+// token has NaN in that dimension in the end.
+constexpr int kNoNan = 0x7fffffff;
+__device__ __forceinline__ void note_nan(int *first_nan, uint32_t nans, int dim, int tok)
+{
+    if (nans) atomicMin(&first_nan[dim], tok + (__builtin_ctz(nans) >> 3));
+}
+
 constexpr float kInf = __builtin_inff();
 
 // 2^x for -inf..; x finite or -inf.
@@ -226,9 +253,11 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
     typedef typename QFrag<kQ>::type Q8;
     __shared__ f32x4 obuf[2][kX][kWave];
     __shared__ float stat[3][kWaves][kRows];
+    __shared__ int first_nan[kD];
 
     Item it;
-    if (!find_item<kRows>(a, blockIdx.x, it)) return;
+    for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
+    if (!find_item<kRows, kTargetFew, kMinTilesFew>(a, blockIdx.x, it)) return;   // has barriers
     const KvView &c = a.c;
     const int ln = lane(), col = ln & 15, g = ln >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(wave());
@@ -289,10 +318,11 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
         for (int x = 0; x < kX; ++x) acc[n][x] = f32x4{0, 0, 0, 0};
     }
 
-    const int t0 = (int)it.first;
-    int t1 = (int)(it.first + it.count);
+    // The tiles that some row sees, in even parts.
     const int see = high < 0 ? 0 : high / kTile + 1;
-    t1 = t1 < see ? t1 : see;
+    const int part = (see + (int)it.splits - 1) / (int)it.splits;
+    const int t0 = (int)it.split * part;
+    const int t1 = t0 + part < see ? t0 + part : see;
     const int last_block = len > 0 ? (len - 1) / kBlock : 0;
     const int32_t *const tab = c.table + (uint64_t)b * c.width;
     const int kblk = col >> 2;              // block of the lane's key rows
@@ -404,52 +434,24 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
             for (int x = 0; x < kX; ++x) acc[n][x] *= back;
         }
 
-        if constexpr (kCodes == DMADESC_KV_E4M3) {
-            // A NaN code that a row does not see must not reach it (0 * NaN):
-            // codes past the length are cleared; other NaN codes are found by
-            // a product of indicators and then cleared.
-            if (edge) {
-                uint32_t found = 0;
+        if (kCodes == DMADESC_KV_E4M3 && edge) {
+            uint32_t found = 0;
+#pragma unroll
+            for (int x = 0; x < kX; ++x)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int keep = nvalid - 4 * q;
-                    const uint32_t mask = keep >= 4 ? 0xffffffffu : keep <= 0 ? 0u : (1u << (8 * keep)) - 1u;
+                    vr[x][q] &= keep_mask(nvalid, q);
+                    found |= nan_bytes(vr[x][q]);
+                }
+            if (__ballot(found != 0)) {
 #pragma unroll
-                    for (int x = 0; x < kX; ++x) {
-                        vr[x][q] &= mask;
-                        found |= nan_bytes(vr[x][q]);
+                for (int x = 0; x < kX; ++x)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t z = nan_bytes(vr[x][q]);
+                        note_nan(first_nan, z, 16 * x + col, tok + 4 * q);
+                        vr[x][q] = without(vr[x][q], z);
                     }
-                }
-                if (__ballot(found != 0)) {
-#pragma unroll
-                    for (int x = 0; x < kX; ++x)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            f16x8 is_nan;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                is_nan[i] = (_Float16)(float)(nan_bytes(vr[x][2 * u + i / 4]) >>
-                                                              (8 * (i & 3) + 7) & 1u);
-#pragma unroll
-                            for (int n = 0; n < kNt; ++n) {
-                                f16x8 seen;
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    seen[i] = (_Float16)(tok + 8 * u + i <= limit[n] ? 1.0f : 0.0f);
-                                const f32x4 cnt = mfma(is_nan, seen, f32x4{0, 0, 0, 0});
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (cnt[i] > 0.0f) acc[n][x][i] = __builtin_nanf("");
-                            }
-                        }
-#pragma unroll
-                    for (int x = 0; x < kX; ++x)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t z = nan_bytes(vr[x][q]);
-                            vr[x][q] &= ~(z | (z - (z >> 7)));
-                        }
-                }
             }
         }
 #pragma unroll
@@ -516,7 +518,12 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
             if (r < nrows) {
 #pragma unroll
                 for (int x = 0; x < kX; ++x) {
-                    const f32x4 o = (acc[n][x] + obuf[0][x][ln]) * norm;
+                    f32x4 o = (acc[n][x] + obuf[0][x][ln]) * norm;
+                    if (kCodes == DMADESC_KV_E4M3) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (first_nan[16 * x + 4 * g + i] <= limit[n]) o[i] = __builtin_nanf("");
+                    }
                     if (whole)
                         store4<kQ>(a.out, orow[n] + 16 * x + 4 * g, o);
                     else
@@ -533,28 +540,303 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
     }
 }
 
+// ------------------------------------------------------------- many rows ---
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// The larger of x in this lane and in the lane 32 away.
+__device__ __forceinline__ float half_max(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Attention for chunks of prompts, where the matrix cores are the bound: a
+// workgroup takes 128 query rows of one key head, 32 a wave, and all of its
+// waves walk the same tiles of 64 tokens. A tile's codes are turned into 16-bit
+// floats once, on the way into LDS (two buffers, one barrier a tile, the loads
+// of the tile after the next in flight meanwhile). As above S^T = K Q^T and
+// O^T = V^T P^T, here with the 32x32x16 product, which reads half the operand
+// bytes per operation that the 16x16x32 one reads. K's tokens are laid in LDS
+// with bits 2 and 3 of their number exchanged: then each lane's scores 8 c ..
+// 8 c + 7 are tokens 8 h .. 8 h + 7 of block c (h = lane / 32), which is the
+// order in which the second product takes them. The running maxima move only
+// when a row's maximum passes its reference by 2^8, so that the accumulators
+// are seldom rescaled; probabilities are therefore scaled by 2^6 here.
+template <int kD, int kQ, int kCodes>
+__global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(AttendArgs a)
+{
+    constexpr int kK = kD / 16;                     // steps of the first product
+    constexpr int kX = kD / 32;                     // 32-dimension pieces of the output
+    constexpr int kChunkStride = kTile * 16 + 16;   // 8 dimensions of 64 tokens, and a bank step
+    constexpr int kLoads = kTile * kD / 16 / kThreads;   // 16-byte loads of a thread, K and V each
+    constexpr float kRise = 8.0f, kLift = 6.0f;
+    typedef typename QFrag<kQ>::type Q8;
+    __shared__ __align__(16) uint8_t kbuf[2][kD / 8 * kChunkStride];
+    __shared__ __align__(16) uint8_t vbuf[2][kTile * kD * 2];
+    __shared__ float scales[2][2][4];               // [buffer][K, V][block]
+    __shared__ int first_nan[kD];
+
+    Item it;
+    for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
+    if (!find_item<kRowsMany, kTargetMany, kMinTilesMany>(a, blockIdx.x, it)) return;   // has barriers
+    const KvView &c = a.c;
+    const int ln = lane(), col = ln & 31, h = ln >> 5, tid = (int)threadIdx.x;
+    const int wv = __builtin_amdgcn_readfirstlane(wave());
+    const uint32_t b = __builtin_amdgcn_readfirstlane(it.b);
+    const uint32_t head = __builtin_amdgcn_readfirstlane(it.head);
+    const uint32_t row0 = __builtin_amdgcn_readfirstlane(it.rt) * kRowsMany;
+    uint32_t s0, s1;
+    kv_span(a.q_start, b, a.total, s0, s1);
+    const int len = kv_len(c, b), news = (int)(s1 - s0);
+    const uint32_t nrows = (uint32_t)news * a.group;
+    const int per = (int)c.tshift - 4;
+    const uint32_t sub_mask = (1u << per) - 1u;
+
+    int low = len - 1, high = len - 1;              // least and largest limit of the tile's rows
+    if (a.causal) {
+        const uint32_t last = nrows - 1 < row0 + kRowsMany - 1 ? nrows - 1 : row0 + kRowsMany - 1;
+        low = len - news + (int)(row0 / a.group);
+        high = len - news + (int)(last / a.group);
+    }
+    const int see = high < 0 ? 0 : high / kTile + 1;
+    const int part = (see + (int)it.splits - 1) / (int)it.splits;
+    const int t0 = (int)it.split * part;
+    const int t1 = t0 + part < see ? t0 + part : see;
+
+    Q8 qf[kK];
+    int limit;
+    uint64_t orow;
+    const uint32_t r = row0 + wv * 32 + col;
+    const bool on = r < nrows;
+    {
+        const uint32_t rr = on ? r : 0u, j = rr / a.group, hq = head * a.group + rr % a.group;
+        limit = !on ? -1 : a.causal ? len - news + (int)j : len - 1;
+        orow = ((uint64_t)(s0 + j) * a.heads + hq) * kD;
+        const uint16_t *const q = static_cast<const uint16_t *>(a.q) +
+                                  (int64_t)(s0 + j) * a.q_tok + (int64_t)hq * a.q_head + 8 * h;
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // a negative scale turns q round
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+            u32x4 w = {0, 0, 0, 0};
+            if (on) w = *reinterpret_cast<const u32x4 *>(q + 16 * k) ^ flip;
+            qf[k] = __builtin_bit_cast(Q8, w);
+        }
+    }
+    const float scale = fabsf(a.scale);
+
+    f32x16 acc[kX];
+#pragma unroll
+    for (int x = 0; x < kX; ++x)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[x][i] = 0.0f;
+    float m = -kInf, mx = -kInf, l = 0.0f;
+
+    // Staging: thread tid loads 16-byte pieces tid, tid + 256, .. of the tile's K
+    // and V; a piece of K is 16 dimensions of a token, of V 16 tokens of a dimension.
+    constexpr int kPieces = kD;                     // 16-byte pieces of a block
+    const int32_t *const tab = c.table + (uint64_t)b * c.width;
+    const int last_block = len > 0 ? (len - 1) / kBlock : 0;
+    u32x4 kr[kLoads], vr[kLoads];
+    float sc = 0.0f;
+    auto block_at = [&](int blk, uint32_t &sub) -> const uint8_t * {
+        const int bb = blk < last_block ? blk : last_block;
+        const int32_t p = tab[bb >> per];
+        sub = (head << per) + ((uint32_t)bb & sub_mask);
+        return c.pool + (uint64_t)((uint32_t)p < c.npages ? (uint32_t)p : 0u) * c.page_bytes;
+    };
+    auto load = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int piece = tid + i * kThreads;
+            uint32_t sub;
+            const uint8_t *const p = block_at(t * 4 + piece / kPieces, sub);
+            const uint8_t *const at = p + (uint64_t)sub * (kBlock * kD) + piece % kPieces * 16;
+            kr[i] = *reinterpret_cast<const u32x4 *>(at);
+            vr[i] = *reinterpret_cast<const u32x4 *>(at + c.code_bytes);
+        }
+        if (tid < 8) {
+            uint32_t sub;
+            const uint8_t *const p = block_at(t * 4 + (tid & 3), sub);
+            sc = reinterpret_cast<const float *>(p + 2ull * c.code_bytes)[(tid >> 2) * c.scales + sub];
+            if ((t * 4 + (tid & 3)) * kBlock >= len) sc = 0.0f;
+        }
+    };
+    auto stage = [&](int t, int buf) {
+        const bool edge = t * kTile + kTile - 1 > low;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int piece = tid + i * kThreads;
+            const int blk = piece / kPieces, in = piece % kPieces;
+            const int tok = in / (kD / 16), x = in % (kD / 16);
+            const int pos = blk * 16 + ((tok & 3) | (tok >> 1 & 4) | (tok << 1 & 8));
+            Q8 *const kd = reinterpret_cast<Q8 *>(kbuf[buf] + 2 * x * kChunkStride + pos * 16);
+            kd[0] = codes8<kCodes, Q8>(kr[i][0], kr[i][1]);
+            *reinterpret_cast<Q8 *>(kbuf[buf] + (2 * x + 1) * kChunkStride + pos * 16) =
+                codes8<kCodes, Q8>(kr[i][2], kr[i][3]);
+            u32x4 w = vr[i];
+            if (kCodes == DMADESC_KV_E4M3 && edge) {
+                const int tok0 = t * kTile + blk * kBlock;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    w[q] &= keep_mask(len - tok0, q);
+                    const uint32_t z = nan_bytes(w[q]);
+                    note_nan(first_nan, z, in, tok0 + 4 * q);
+                    w[q] = without(w[q], z);
+                }
+            }
+            f16x8 *const vd = reinterpret_cast<f16x8 *>(vbuf[buf]) + blk * 2 * kD + in;
+            vd[0] = codes8<kCodes, f16x8>(w[0], w[1]);
+            vd[kD] = codes8<kCodes, f16x8>(w[2], w[3]);
+        }
+        if (tid < 8) scales[buf][tid >> 2][tid & 3] = sc;
+    };
+
+    if (t0 < t1) {
+        load(t0);
+        stage(t0, 0);
+        if (t0 + 1 < t1) load(t0 + 1);
+    }
+    for (int t = t0; t < t1; ++t) {
+        const int buf = (t - t0) & 1;
+        __syncthreads();                            // tile t is whole, tile t - 1 read
+        if (t + 1 < t1) {
+            stage(t + 1, buf ^ 1);
+            if (t + 2 < t1) load(t + 2);
+        }
+        f32x16 s[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kK; ++k) {
+                const Q8 kf = *reinterpret_cast<const Q8 *>(kbuf[buf] + (2 * k + h) * kChunkStride +
+                                                            (u * 32 + col) * 16);
+                s[u] = mfma32(kf, qf[k], s[u]);
+            }
+        }
+        const bool edge = t * kTile + kTile - 1 > low;
+        if (edge) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int tok = t * kTile + u * 32 + (i >> 3) * 16 + 8 * h + (i & 7);
+                    s[u][i] = tok <= limit ? s[u][i] : -kInf;
+                }
+        }
+        float ks[4], vs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // Never 0, so that a masked -inf stays one (blocks past the length have scale 0).
+            ks[i] = fmaxf(scales[buf][0][i] * scale, 1.17549435e-38f);
+            vs[i] = scales[buf][1][i];
+        }
+        float top = -kInf, topv = -kInf;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v = -kInf;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v = fmaxf(v, s[i >> 1][(i & 1) * 8 + k]);
+            v *= ks[i];
+            top = fmaxf(top, v);
+            topv = fmaxf(topv, v + (float)((int)(__float_as_uint(vs[i]) >> 23 & 0xffu) - 126));
+        }
+        top = half_max(top);
+        topv = half_max(topv);
+        if (__ballot(top > m + kRise || topv > mx + kRise)) {
+            const float mn = fmaxf(m, top), mxn = fmaxf(mx, topv);
+            const float back = mxn == -kInf ? 1.0f : exp2_(mx - mxn);
+            l *= mn == -kInf ? 1.0f : exp2_(m - mn);
+            m = mn;
+            mx = mxn;
+#pragma unroll
+            for (int x = 0; x < kX; ++x) acc[x] *= back;
+        }
+        const float ms = m == -kInf ? 0.0f : m;
+        const float shift = ms - (mx == -kInf ? 0.0f : mx) + kLift;
+        const float lift = exp2_(shift);
+        f16x8 pf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = vs[i] * lift;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float p = exp2_(__builtin_fmaf(s[i >> 1][(i & 1) * 8 + k], ks[i], -ms));
+                l += p;
+                pf[i][k] = (_Float16)(p * f);
+            }
+        }
+        const f16x8 *const vb = reinterpret_cast<const f16x8 *>(vbuf[buf]) + h * kD + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int x = 0; x < kX; ++x)
+                acc[x] = mfma32(vb[i * 2 * kD + x * 32], pf[i], acc[x]);
+    }
+
+    if (blockIdx.x == it.base && tid == 0) a.plan[b] = make_uint2(it.base, it.splits);
+    l += __shfl_xor(l, 32, kWave);
+    if (!on) return;
+    const float ms = m == -kInf ? 0.0f : m, mxs = mx == -kInf ? 0.0f : mx;
+    const float norm = l == 0.0f ? 0.0f : exp2_(mxs - ms - kLift) / l;
+    const float lse2 = l == 0.0f ? -kInf : ms + __builtin_log2f(l);
+    const uint64_t prow = (uint64_t)blockIdx.x * kRowsMany + wv * 32 + col;
+#pragma unroll
+    for (int x = 0; x < kX; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x4 o = f32x4{acc[x][4 * i], acc[x][4 * i + 1], acc[x][4 * i + 2],
+                            acc[x][4 * i + 3]} * norm;
+            const int d = 32 * x + 8 * i + 4 * h;
+            if (kCodes == DMADESC_KV_E4M3) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (first_nan[d + k] <= limit) o[k] = __builtin_nanf("");
+            }
+            if (it.splits == 1) store4<kQ>(a.out, orow + d, o);
+            else *reinterpret_cast<f32x4 *>(a.part + prow * kD + d) = o;
+        }
+    if (h == 0) {
+        if (it.splits != 1) a.part_lse[prow] = lse2;
+        else if (a.lse) a.lse[orow / kD] = lse2 * 0.69314718055994531f;
+    }
+}
+
 // Joins the splits of one output row (token, head): a workgroup's waves take
 // every fourth split each.
 template <int kD, int kQ>
-__global__ __launch_bounds__(kThreads) void k_kv_join(AttendArgs a, uint32_t tile_rows)
+__global__ __launch_bounds__(kThreads) void k_kv_join(AttendArgs few, AttendArgs many,
+                                                     uint32_t tile_rows)
 {
     constexpr int kE = kD / kWave;          // values of a lane
     __shared__ float part[kWaves][kD];
     __shared__ float mass[kWaves];
-    const uint32_t tokn = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
-    const uint32_t b = kv_request_of(a.c.rows, tokn, [&](uint32_t r) {
-        const int32_t s = a.q_start[r];
+    const uint32_t tokn = blockIdx.x / few.heads, h = blockIdx.x % few.heads;
+    const uint32_t b = kv_request_of(few.c.rows, tokn, [&](uint32_t r) {
+        const int32_t s = few.q_start[r];
         return (uint64_t)(s < 0 ? 0 : s);
     });
     uint32_t s0, s1;
-    kv_span(a.q_start, b, a.total, s0, s1);
+    kv_span(few.q_start, b, few.total, s0, s1);
     if (tokn < s0 || tokn >= s1) return;
+    const bool is_many = (s1 - s0) * few.group > few.most;
+    const AttendArgs &a = is_many ? many : few;
+    if (is_many) tile_rows = kRowsMany;
     const uint2 plan = a.plan[b];
     if (plan.y <= 1 || plan.y > kMaxSplits) return;
     const uint32_t kvh = h / a.group;
     const uint32_t r = (tokn - s0) * a.group + h % a.group;
     const uint32_t rts = ((s1 - s0) * a.group + tile_rows - 1) / tile_rows;
-    const uint32_t first = plan.x + kvh * rts + r / tile_rows, step = a.c.kv_heads * rts;
+    const uint32_t first = plan.x + r / tile_rows * a.c.kv_heads + kvh, step = a.c.kv_heads * rts;
     if ((uint64_t)first + (uint64_t)(plan.y - 1) * step >= a.slots) return;   // q_start out of order
     const uint64_t in = r % tile_rows;
     float top = -kInf;
@@ -588,86 +870,124 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(AttendArgs a, uint32_t til
         a.lse[blockIdx.x] = all == 0.0f ? -kInf : (top + __builtin_log2f(all)) * 0.69314718055994531f;
 }
 
-// Rows of a tile: one product's 16 where a request's rows fit it, else 32.
+// Rows of a tile of the kernel of few rows: one product's 16 where a request's
+// rows fit it, else 32.
 uint32_t tile_rows_of(uint64_t total, uint32_t rows, uint32_t group)
 {
     return (total + rows - 1) / rows * group <= 16 ? 16u : 32u;
 }
 
-// Workgroups (= partial results) that a call may need: the even pieces, and
-// one more for each row tile of each key head.
-uint64_t slots_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads)
+// How a call's memory and launches follow from what the host knows.
+struct Launch {
+    uint32_t tile_rows;          // of the kernel of few rows
+    uint32_t few, many;          // workgroups (= partial results) of each kernel
+    bool join;
+    size_t plan_at, few_lse, few_part, many_lse, many_part, bytes;
+};
+
+Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads, uint32_t dim,
+                 uint64_t tokens)
 {
-    const uint32_t group = heads / kv_heads, tr = tile_rows_of(total, rows, group);
-    return kTarget + kv_heads * (total * group / tr + rows);
+    Launch p{};
+    const uint32_t group = heads / kv_heads;
+    p.tile_rows = tile_rows_of(total, rows, group);
+    // The even pieces, and one more for each row tile of each key head. A
+    // request's rows are many only if all rows together are; a call's only
+    // request has all of them.
+    const bool many = total * group > kMostFew;
+    const uint64_t most = (tokens + kTile - 1) / kTile;
+    const bool split_few = most > kMinTilesFew, split_many = most > kMinTilesMany;
+    if (!(many && rows == 1))
+        p.few = (uint32_t)((split_few ? kTargetFew : 0u) +
+                           kv_heads * (total * group / p.tile_rows + rows));
+    if (many)
+        p.many = (uint32_t)((split_many ? kTargetMany : 0u) +
+                            kv_heads * (total * group / kRowsMany +
+                                        (total * group / (kMostFew + 1) < rows
+                                             ? total * group / (kMostFew + 1) : rows)));
+    p.join = (p.few && split_few) || (p.many && split_many);
+    size_t at = align256(8ull * rows);
+    auto take = [&](size_t bytes) { const size_t r = at; at += align256(bytes); return r; };
+    const size_t f = split_few ? p.few : 0, n = split_many ? p.many : 0;
+    p.few_lse = take(4 * f * p.tile_rows);
+    p.few_part = take(4 * f * p.tile_rows * dim);
+    p.many_lse = take(4 * n * kRowsMany);
+    p.many_part = take(4 * n * kRowsMany * dim);
+    p.bytes = at;
+    return p;
 }
 
 template <int kD, int kQ, int kCodes>
-void launch_rows(const AttendArgs &a, uint32_t tile_rows, uint32_t grid, hipStream_t s)
+void launch_all(const AttendArgs &few, const AttendArgs &many, const Launch &p, hipStream_t s)
 {
-    if (tile_rows == 16) k_kv_attend<kD, kQ, kCodes, 1><<<grid, kThreads, 0, s>>>(a);
-    else k_kv_attend<kD, kQ, kCodes, 2><<<grid, kThreads, 0, s>>>(a);
-}
-
-template <int kD, int kQ>
-void launch_codes(const AttendArgs &a, uint32_t codes, uint32_t tile_rows, uint32_t grid,
-                  bool join, hipStream_t s)
-{
-    if (codes == DMADESC_KV_E4M3) launch_rows<kD, kQ, DMADESC_KV_E4M3>(a, tile_rows, grid, s);
-    else launch_rows<kD, kQ, DMADESC_KV_INT8>(a, tile_rows, grid, s);
-    if (join) k_kv_join<kD, kQ><<<a.total * a.heads, kThreads, 0, s>>>(a, tile_rows);
+    if (p.many) k_kv_attend_many<kD, kQ, kCodes><<<p.many, kThreads, 0, s>>>(many);
+    if (p.few) {
+        if (p.tile_rows == 16) k_kv_attend<kD, kQ, kCodes, 1><<<p.few, kThreads, 0, s>>>(few);
+        else k_kv_attend<kD, kQ, kCodes, 2><<<p.few, kThreads, 0, s>>>(few);
+    }
+    if (p.join)
+        k_kv_join<kD, kQ><<<few.total * few.heads, kThreads, 0, s>>>(few, many, p.tile_rows);
 }
 
 template <int kD>
-void launch_type(const AttendArgs &a, uint32_t type, uint32_t codes, uint32_t tile_rows,
-                 uint32_t grid, bool join, hipStream_t s)
+void launch_dim(const KvAttendArgs &k, const AttendArgs &few, const AttendArgs &many,
+                const Launch &p, hipStream_t s)
 {
-    if (type == DMADESC_KV_BF16)
-        launch_codes<kD, DMADESC_KV_BF16>(a, codes, tile_rows, grid, join, s);
-    else
-        launch_codes<kD, DMADESC_KV_FP16>(a, codes, tile_rows, grid, join, s);
+    const bool e4m3 = k.cache.codes == DMADESC_KV_E4M3;
+    if (k.type == DMADESC_KV_BF16) {
+        if (e4m3) launch_all<kD, DMADESC_KV_BF16, DMADESC_KV_E4M3>(few, many, p, s);
+        else launch_all<kD, DMADESC_KV_BF16, DMADESC_KV_INT8>(few, many, p, s);
+    } else {
+        if (e4m3) launch_all<kD, DMADESC_KV_FP16, DMADESC_KV_E4M3>(few, many, p, s);
+        else launch_all<kD, DMADESC_KV_FP16, DMADESC_KV_INT8>(few, many, p, s);
+    }
 }
 
 }  // namespace
 
 size_t ws_kv_attend(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads,
-                    uint32_t dim, uint64_t)
+                    uint32_t dim, uint64_t tokens)
 {
     if (total == 0 || rows == 0) return 0;
-    const uint64_t slots = slots_of(total, rows, heads, kv_heads);
-    const uint32_t tr = tile_rows_of(total, rows, heads / kv_heads);
-    return align256(8ull * rows) + align256(4 * slots * tr) + align256(4 * slots * tr * dim);
+    return launch_of(total, rows, heads, kv_heads, dim, tokens).bytes;
 }
 
 hipError_t launch_kv_attend(const KvAttendArgs &k, hipStream_t s)
 {
-    AttendArgs a{};
-    a.c = kv_view(k.cache);
-    if (a.c.npages == 0) a.c.width = 0;                 // no page: every length is 0
-    a.q = k.q;
-    a.q_tok = k.q_tok;
-    a.q_head = k.q_head;
-    a.q_start = k.q_start;
-    a.total = (uint32_t)k.total;
-    a.heads = k.heads;
-    a.group = k.heads / k.cache.kv_heads;
-    a.causal = k.causal;
-    const float scale = k.scale != 0.0f ? k.scale : 1.0f / sqrtf((float)k.cache.dim);
-    a.scale = scale * 1.44269504088896341f;
-    a.out = k.out;
-    a.lse = k.lse;
-    const uint32_t tr = tile_rows_of(k.total, k.cache.rows, a.group);
-    a.slots = (uint32_t)slots_of(k.total, k.cache.rows, k.heads, k.cache.kv_heads);
-    uint8_t *p = static_cast<uint8_t *>(k.ws);
-    a.plan = reinterpret_cast<uint2 *>(p);
-    p += align256(8ull * k.cache.rows);
-    a.part_lse = reinterpret_cast<float *>(p);
-    p += align256(4ull * a.slots * tr);
-    a.part = reinterpret_cast<float *>(p);
-    const bool join = ((uint64_t)a.c.width << a.c.tshift) > (uint64_t)kMinTiles * kTile;
-    if (k.cache.dim == 64) launch_type<64>(a, k.type, k.cache.codes, tr, a.slots, join, s);
-    else if (k.cache.dim == 128) launch_type<128>(a, k.type, k.cache.codes, tr, a.slots, join, s);
-    else launch_type<256>(a, k.type, k.cache.codes, tr, a.slots, join, s);
+    const dmadesc_kv_cache &c = k.cache;
+    const Launch p = launch_of(k.total, c.rows, k.heads, c.kv_heads, c.dim,
+                               (uint64_t)c.width * c.page_tokens);
+    AttendArgs few{};
+    few.c = kv_view(c);
+    if (few.c.npages == 0) few.c.width = 0;             // no page: every length is 0
+    few.q = k.q;
+    few.q_tok = k.q_tok;
+    few.q_head = k.q_head;
+    few.q_start = k.q_start;
+    few.total = (uint32_t)k.total;
+    few.heads = k.heads;
+    few.group = k.heads / c.kv_heads;
+    few.causal = k.causal;
+    const float scale = k.scale != 0.0f ? k.scale : 1.0f / sqrtf((float)c.dim);
+    few.scale = scale * 1.44269504088896341f;
+    few.out = k.out;
+    few.lse = k.lse;
+    uint8_t *const ws = static_cast<uint8_t *>(k.ws);
+    few.plan = reinterpret_cast<uint2 *>(ws + p.plan_at);
+    AttendArgs many = few;
+    few.part = reinterpret_cast<float *>(ws + p.few_part);
+    few.part_lse = reinterpret_cast<float *>(ws + p.few_lse);
+    few.slots = p.few;
+    few.least = 1;
+    few.most = kMostFew;
+    many.part = reinterpret_cast<float *>(ws + p.many_part);
+    many.part_lse = reinterpret_cast<float *>(ws + p.many_lse);
+    many.slots = p.many;
+    many.least = kMostFew + 1;
+    many.most = ~0u;
+    if (c.dim == 64) launch_dim<64>(k, few, many, p, s);
+    else if (c.dim == 128) launch_dim<128>(k, few, many, p, s);
+    else launch_dim<256>(k, few, many, p, s);
     return hipGetLastError();
 }
 
