@@ -561,38 +561,50 @@ __device__ __forceinline__ float half_max(float x)
 // Attention for chunks of prompts, where the matrix cores are the bound: a
 // workgroup takes 128 query rows of one key head, 32 a wave, and all of its
 // waves walk the same tiles of 64 tokens. A tile's codes are turned into 16-bit
-// floats once, on the way into LDS (two buffers, one barrier a tile, the loads
-// of the tile after the next in flight meanwhile). As above S^T = K Q^T and
+// floats once, on the way into LDS (two buffers each, one barrier a tile, the
+// loads of later tiles in flight meanwhile). As above S^T = K Q^T and
 // O^T = V^T P^T, here with the 32x32x16 product, which reads half the operand
 // bytes per operation that the 16x16x32 one reads. K's tokens are laid in LDS
 // with bits 2 and 3 of their number exchanged: then each lane's scores 8 c ..
 // 8 c + 7 are tokens 8 h .. 8 h + 7 of block c (h = lane / 32), which is the
-// order in which the second product takes them. The running maxima move only
-// when a row's maximum passes its reference by 2^8, so that the accumulators
-// are seldom rescaled; probabilities are therefore scaled by 2^6 here.
+// order in which the second product takes them.
+//
+// Here the vector unit has as much to do as the matrix unit, so that two things
+// are done differently. The softmax takes one reference per row, the running
+// maximum M of s + e: 2^(s + e - M + 6) is both the f16 probability and, times
+// 2^-e once per block, the term of the sum; it moves only when a row passes it
+// by 2^8, so that the accumulators are seldom rescaled. (Where scales lie
+// beyond 2^-40..2^40 a term could vanish in the one and matter in the other;
+// from the first such tile on the sum is taken from exponentials of its own.)
+// And the loop is skewed: the next tile's scores are multiplied while this
+// tile's exponentials are taken, and the next codes converted under the product
+// with V.
 template <int kD, int kQ, int kCodes>
 __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(AttendArgs a)
 {
     constexpr int kK = kD / 16;                     // steps of the first product
     constexpr int kX = kD / 32;                     // 32-dimension pieces of the output
+    constexpr int kRows = (int)kRowsMany;
     constexpr int kChunkStride = kTile * 16 + 16;   // 8 dimensions of 64 tokens, and a bank step
     constexpr int kLoads = kTile * kD / 16 / kThreads;   // 16-byte loads of a thread, K and V each
+    constexpr int kPieces = kD;                     // 16-byte pieces of a block
     constexpr float kRise = 8.0f, kLift = 6.0f;
     typedef typename QFrag<kQ>::type Q8;
     __shared__ __align__(16) uint8_t kbuf[2][kD / 8 * kChunkStride];
     __shared__ __align__(16) uint8_t vbuf[2][kTile * kD * 2];
-    __shared__ float scales[2][2][4];               // [buffer][K, V][block]
+    __shared__ float scales[2][3][4];   // [buffer][scale of K, exponent of V, 2^-that][block]
     __shared__ int first_nan[kD];
 
     Item it;
     for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
-    if (!find_item<kRowsMany, kTargetMany, kMinTilesMany>(a, blockIdx.x, it)) return;   // has barriers
+    if (!find_item<kRows, kTargetMany, kMinTilesMany>(a, blockIdx.x, it)) return;   // has barriers
     const KvView &c = a.c;
     const int ln = lane(), col = ln & 31, h = ln >> 5, tid = (int)threadIdx.x;
     const int wv = __builtin_amdgcn_readfirstlane(wave());
     const uint32_t b = __builtin_amdgcn_readfirstlane(it.b);
     const uint32_t head = __builtin_amdgcn_readfirstlane(it.head);
-    const uint32_t row0 = __builtin_amdgcn_readfirstlane(it.rt) * kRowsMany;
+    const uint32_t row0 = __builtin_amdgcn_readfirstlane(it.rt) * kRows;
+    const uint32_t wrow0 = row0 + wv * 32;   // first row of the wave
     uint32_t s0, s1;
     kv_span(a.q_start, b, a.total, s0, s1);
     const int len = kv_len(c, b), news = (int)(s1 - s0);
@@ -600,11 +612,13 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
     const int per = (int)c.tshift - 4;
     const uint32_t sub_mask = (1u << per) - 1u;
 
-    int low = len - 1, high = len - 1;              // least and largest limit of the tile's rows
+    // Least and largest limit of the workgroup's rows, least of the wave's.
+    int low = len - 1, high = len - 1, wlow = len - 1;
     if (a.causal) {
-        const uint32_t last = nrows - 1 < row0 + kRowsMany - 1 ? nrows - 1 : row0 + kRowsMany - 1;
+        const uint32_t last = nrows - 1 < row0 + kRows - 1 ? nrows - 1 : row0 + kRows - 1;
         low = len - news + (int)(row0 / a.group);
         high = len - news + (int)(last / a.group);
+        wlow = len - news + (int)(wrow0 / a.group);
     }
     const int see = high < 0 ? 0 : high / kTile + 1;
     const int part = (see + (int)it.splits - 1) / (int)it.splits;
@@ -612,16 +626,13 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
     const int t1 = t0 + part < see ? t0 + part : see;
 
     Q8 qf[kK];
-    int limit;
-    uint64_t orow;
-    const uint32_t r = row0 + wv * 32 + col;
+    const uint32_t r = wrow0 + col;
     const bool on = r < nrows;
+    const uint32_t jq = on ? r / a.group : 0u, hq = head * a.group + (on ? r % a.group : 0u);
+    const int limit = !on ? -1 : a.causal ? len - news + (int)jq : len - 1;
     {
-        const uint32_t rr = on ? r : 0u, j = rr / a.group, hq = head * a.group + rr % a.group;
-        limit = !on ? -1 : a.causal ? len - news + (int)j : len - 1;
-        orow = ((uint64_t)(s0 + j) * a.heads + hq) * kD;
         const uint16_t *const q = static_cast<const uint16_t *>(a.q) +
-                                  (int64_t)(s0 + j) * a.q_tok + (int64_t)hq * a.q_head + 8 * h;
+                                  (int64_t)(s0 + jq) * a.q_tok + (int64_t)hq * a.q_head + 8 * h;
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // a negative scale turns q round
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
@@ -637,94 +648,169 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
     for (int x = 0; x < kX; ++x)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[x][i] = 0.0f;
-    float m = -kInf, mx = -kInf, l = 0.0f;
+    float mx = -kInf, l = 0.0f;
 
     // Staging: thread tid loads 16-byte pieces tid, tid + 256, .. of the tile's K
-    // and V; a piece of K is 16 dimensions of a token, of V 16 tokens of a dimension.
-    constexpr int kPieces = kD;                     // 16-byte pieces of a block
+    // and V; a piece of K is 16 dimensions of a token, of V 16 tokens of a
+    // dimension. A wave's 64 pieces lie in one block, so its page and address are
+    // scalars, read from the lanes of a register that holds the pages of 64 blocks;
+    // the next 64 are loaded 16 tiles ahead. Tiles past the last are staged too
+    // (from addresses inside a page) and not used.
     const int32_t *const tab = c.table + (uint64_t)b * c.width;
     const int last_block = len > 0 ? (len - 1) / kBlock : 0;
     u32x4 kr[kLoads], vr[kLoads];
     float sc = 0.0f;
-    auto block_at = [&](int blk, uint32_t &sub) -> const uint8_t * {
-        const int bb = blk < last_block ? blk : last_block;
-        const int32_t p = tab[bb >> per];
-        sub = (head << per) + ((uint32_t)bb & sub_mask);
-        return c.pool + (uint64_t)((uint32_t)p < c.npages ? (uint32_t)p : 0u) * c.page_bytes;
+    int group = t0;                                 // tile of lane 0 of `here`; `ahead` follows it
+    int32_t here, ahead;
+    auto load_pages = [&](int t) -> int32_t {
+        const int blk = t * 4 + ln;
+        const uint32_t p = (uint32_t)tab[(blk < last_block ? blk : last_block) >> per];
+        return (int32_t)(p < c.npages ? p : 0u);
     };
-    auto load = [&](int t) {
+    auto piece_at = [&](int t, int i) -> const uint8_t * {
+        const int first = wv * kWave + i * kThreads, blk = first / kPieces;
+        const int32_t p = __builtin_amdgcn_readlane(here, (t - group) * 4 + blk);
+        const uint32_t sub = (head << per) + ((uint32_t)(t * 4 + blk) & sub_mask);
+        return c.pool + (uint64_t)(uint32_t)p * c.page_bytes + (uint64_t)sub * (kBlock * kD) +
+               first % kPieces * 16;
+    };
+    auto load_k = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int piece = tid + i * kThreads;
-            uint32_t sub;
-            const uint8_t *const p = block_at(t * 4 + piece / kPieces, sub);
-            const uint8_t *const at = p + (uint64_t)sub * (kBlock * kD) + piece % kPieces * 16;
-            kr[i] = *reinterpret_cast<const u32x4 *>(at);
-            vr[i] = *reinterpret_cast<const u32x4 *>(at + c.code_bytes);
-        }
-        if (tid < 8) {
-            uint32_t sub;
-            const uint8_t *const p = block_at(t * 4 + (tid & 3), sub);
-            sc = reinterpret_cast<const float *>(p + 2ull * c.code_bytes)[(tid >> 2) * c.scales + sub];
-            if ((t * 4 + (tid & 3)) * kBlock >= len) sc = 0.0f;
+        for (int i = 0; i < kLoads; ++i)
+            kr[i] = *reinterpret_cast<const u32x4 *>(piece_at(t, i) + ln * 16);
+    };
+    auto load_v = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            vr[i] = *reinterpret_cast<const u32x4 *>(piece_at(t, i) + c.code_bytes + ln * 16);
+        if (wv == 0) {                              // lanes 0..7: K's and V's scales of the 4 blocks
+            const uint32_t p = (uint32_t)__shfl(here, (t - group) * 4 + (ln & 3), kWave);
+            const uint32_t sub = (head << per) + ((uint32_t)(t * 4 + (ln & 3)) & sub_mask);
+            if (ln < 8)
+                sc = reinterpret_cast<const float *>(c.pool + (uint64_t)p * c.page_bytes +
+                                                     2ull * c.code_bytes)[(ln >> 2) * c.scales + sub];
         }
     };
-    auto stage = [&](int t, int buf) {
-        const bool edge = t * kTile + kTile - 1 > low;
+    auto clean_v = [&](int t) {                     // the tile's codes that must not count
+        if (kCodes == DMADESC_KV_E4M3 && t * kTile + kTile - 1 > low) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int piece = tid + i * kThreads;
-            const int blk = piece / kPieces, in = piece % kPieces;
-            const int tok = in / (kD / 16), x = in % (kD / 16);
-            const int pos = blk * 16 + ((tok & 3) | (tok >> 1 & 4) | (tok << 1 & 8));
-            Q8 *const kd = reinterpret_cast<Q8 *>(kbuf[buf] + 2 * x * kChunkStride + pos * 16);
-            kd[0] = codes8<kCodes, Q8>(kr[i][0], kr[i][1]);
-            *reinterpret_cast<Q8 *>(kbuf[buf] + (2 * x + 1) * kChunkStride + pos * 16) =
-                codes8<kCodes, Q8>(kr[i][2], kr[i][3]);
-            u32x4 w = vr[i];
-            if (kCodes == DMADESC_KV_E4M3 && edge) {
-                const int tok0 = t * kTile + blk * kBlock;
+            for (int i = 0; i < kLoads; ++i) {
+                const int piece = tid + i * kThreads, in = piece % kPieces;
+                const int tok0 = t * kTile + piece / kPieces * kBlock;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    w[q] &= keep_mask(len - tok0, q);
-                    const uint32_t z = nan_bytes(w[q]);
+                    vr[i][q] &= keep_mask(len - tok0, q);
+                    const uint32_t z = nan_bytes(vr[i][q]);
                     note_nan(first_nan, z, in, tok0 + 4 * q);
-                    w[q] = without(w[q], z);
+                    vr[i][q] = without(vr[i][q], z);
                 }
             }
-            f16x8 *const vd = reinterpret_cast<f16x8 *>(vbuf[buf]) + blk * 2 * kD + in;
-            vd[0] = codes8<kCodes, f16x8>(w[0], w[1]);
-            vd[kD] = codes8<kCodes, f16x8>(w[2], w[3]);
         }
-        if (tid < 8) scales[buf][tid >> 2][tid & 3] = sc;
     };
-
-    if (t0 < t1) {
-        load(t0);
-        stage(t0, 0);
-        if (t0 + 1 < t1) load(t0 + 1);
-    }
-    for (int t = t0; t < t1; ++t) {
-        const int buf = (t - t0) & 1;
-        __syncthreads();                            // tile t is whole, tile t - 1 read
-        if (t + 1 < t1) {
-            stage(t + 1, buf ^ 1);
-            if (t + 2 < t1) load(t + 2);
+    // Half n of the thread's pieces (8 codes each): K's, then V's.
+    constexpr int kOps = 4 * kLoads;
+    auto stage = [&](int buf, int n) {
+        const int i = n >> 1 & (kLoads - 1), piece = tid + i * kThreads;
+        const int blk = piece / kPieces, in = piece % kPieces;
+        if (n < kOps / 2) {
+            const int tok = in / (kD / 16), x = in % (kD / 16);
+            const int pos = blk * 16 + ((tok & 3) | (tok >> 1 & 4) | (tok << 1 & 8));
+            *reinterpret_cast<Q8 *>(kbuf[buf] + (2 * x + (n & 1)) * kChunkStride + pos * 16) =
+                codes8<kCodes, Q8>(kr[i][2 * (n & 1)], kr[i][2 * (n & 1) + 1]);
+        } else {
+            reinterpret_cast<f16x8 *>(vbuf[buf])[(blk * 2 + (n & 1)) * kD + in] =
+                codes8<kCodes, f16x8>(vr[i][2 * (n & 1)], vr[i][2 * (n & 1) + 1]);
         }
-        f32x16 s[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kK; ++k) {
-                const Q8 kf = *reinterpret_cast<const Q8 *>(kbuf[buf] + (2 * k + h) * kChunkStride +
-                                                            (u * 32 + col) * 16);
-                s[u] = mfma32(kf, qf[k], s[u]);
+    };
+    auto stage_scales = [&](int t, int buf) {
+        if (tid < 8) {                              // K: scale; V: exponent and 2^-exponent
+            const float s = (t * 4 + (tid & 3)) * kBlock < len ? sc : 1.0f;
+            const int e = (int)(__float_as_uint(s) >> 23 & 0xffu) - 127;
+            if (tid < 4) {
+                // Never 0, so that a masked -inf stays one.
+                scales[buf][0][tid] = fmaxf(s * scale, 1.17549435e-38f);
+            } else {
+                scales[buf][1][tid - 4] = (float)e;
+                scales[buf][2][tid - 4] = __uint_as_float((uint32_t)(e < 127 ? 127 - e : 1) << 23);
             }
         }
-        const bool edge = t * kTile + kTile - 1 > low;
-        if (edge) {
+    };
+    auto k_operand = [&](int buf, int k) -> Q8 {
+        return *reinterpret_cast<const Q8 *>(kbuf[buf] + (2 * (k >> 1) + h) * kChunkStride +
+                                             ((k & 1) * 32 + col) * 16);
+    };
+    auto v_operand = [&](int buf, int k) -> f16x8 {
+        return reinterpret_cast<const f16x8 *>(vbuf[buf])[(k / kX * 2 + h) * kD + k % kX * 32 + col];
+    };
+    auto fetch = [&](int t) {                       // tile t's codes, of this group of 16 or the next
+        if (t >= group + 16) {
+            group += 16;
+            here = ahead;
+            ahead = load_pages(group + 16);
+        }
+        load_k(t);
+        load_v(t);
+    };
+
+    bool wide = false;                              // scales too far apart for one exponential
+    if (t0 < t1) {
+        here = load_pages(t0);
+        ahead = load_pages(t0 + 16);
+        load_k(t0);
+        load_v(t0);
+        clean_v(t0);
+#pragma unroll
+        for (int n = 0; n < kOps; ++n) stage(0, n);
+        stage_scales(t0, 0);
+        fetch(t0 + 1);
+    }
+    if (wrow0 >= nrows) {                           // a wave past the last row only stages
+        for (int t = t0; t < t1; ++t) {
+            const int buf = (t - t0) & 1;
+            __syncthreads();
+            clean_v(t + 1);
+#pragma unroll
+            for (int n = 0; n < kOps; ++n) stage(buf ^ 1, n);
+            stage_scales(t + 1, buf ^ 1);
+            fetch(t + 2);
+        }
+        return;
+    }
+    // In LDS as tile t begins: its codes; in registers: those of t + 1.
+    for (int t = t0; t < t1; ++t) {
+        const int buf = (t - t0) & 1;
+        Q8 kf[4];
+        f16x8 vf[4];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) kf[k] = k_operand(buf, k);
+        clean_v(t + 1);
+        // The scores, the next codes' conversion under them.
+        f32x16 s[2];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[0][i] = s[1][i] = 0.0f;
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int kSteps = 2 * kK;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            if (k + 3 < kSteps) kf[(k + 3) & 3] = k_operand(buf, k + 3);
+            else vf[k + 3 - kSteps] = v_operand(buf, k + 3 - kSteps);
+            s[k & 1] = mfma32(kf[k & 3], qf[k >> 1], s[k & 1]);
+#pragma unroll
+            for (int m = k * kOps / kSteps; m < (k + 1) * kOps / kSteps; ++m) stage(buf ^ 1, m);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        stage_scales(t + 1, buf ^ 1);
+        fetch(t + 2);
+        float ks[4], ve[4], back[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ks[i] = scales[buf][0][i];
+            ve[i] = scales[buf][1][i];
+            back[i] = scales[buf][2][i];
+            wide |= fabsf(ve[i]) > 40.0f;
+        }
+        if (t * kTile + kTile - 1 > wlow) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -733,63 +819,70 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
                     s[u][i] = tok <= limit ? s[u][i] : -kInf;
                 }
         }
-        float ks[4], vs[4];
+        // The reference moves where a row's maximum has risen far enough.
+        float tv = -kInf;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // Never 0, so that a masked -inf stays one (blocks past the length have scale 0).
-            ks[i] = fmaxf(scales[buf][0][i] * scale, 1.17549435e-38f);
-            vs[i] = scales[buf][1][i];
-        }
-        float top = -kInf, topv = -kInf;
+            float top = -kInf;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v = -kInf;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v = fmaxf(v, s[i >> 1][(i & 1) * 8 + k]);
-            v *= ks[i];
-            top = fmaxf(top, v);
-            topv = fmaxf(topv, v + (float)((int)(__float_as_uint(vs[i]) >> 23 & 0xffu) - 126));
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, s[i >> 1][(i & 1) * 8 + k]);
+            tv = fmaxf(tv, __builtin_fmaf(top, ks[i], ve[i]));
         }
-        top = half_max(top);
-        topv = half_max(topv);
-        if (__ballot(top > m + kRise || topv > mx + kRise)) {
-            const float mn = fmaxf(m, top), mxn = fmaxf(mx, topv);
-            const float back = mxn == -kInf ? 1.0f : exp2_(mx - mxn);
-            l *= mn == -kInf ? 1.0f : exp2_(m - mn);
-            m = mn;
+        tv = half_max(tv);
+        if (__ballot(tv > mx + kRise)) {
+            const float mxn = fmaxf(mx, tv);
+            const float by = mxn == -kInf ? 1.0f : exp2_(mx - mxn);
+            l *= by;
             mx = mxn;
 #pragma unroll
-            for (int x = 0; x < kX; ++x) acc[x] *= back;
+            for (int x = 0; x < kX; ++x) acc[x] *= by;
         }
-        const float ms = m == -kInf ? 0.0f : m;
-        const float shift = ms - (mx == -kInf ? 0.0f : mx) + kLift;
-        const float lift = exp2_(shift);
-        f16x8 pf[4];
+        const float ref = (mx == -kInf ? 0.0f : mx) - kLift;
+        if (__builtin_amdgcn_readfirstlane(wide)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float f = vs[i] * lift;
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float p = exp2_(__builtin_fmaf(s[i >> 1][(i & 1) * 8 + k], ks[i], -ms));
-                l += p;
-                pf[i][k] = (_Float16)(p * f);
+                for (int k = 0; k < 8; ++k)
+                    l += exp2_(__builtin_fmaf(s[i >> 1][(i & 1) * 8 + k], ks[i], -ref));
+                back[i] = 0.0f;
             }
         }
-        const f16x8 *const vb = reinterpret_cast<const f16x8 *>(vbuf[buf]) + h * kD + col;
+        // The exponentials of block i + 1 under block i's product with V.
+        f16x8 pf[2];
+        float sum = 0.0f;
+        auto take = [&](int i, int k) {
+            const float p = exp2_(__builtin_fmaf(s[i >> 1][(i & 1) * 8 + k], ks[i], ve[i] - ref));
+            sum += p;
+            pf[i & 1][k] = (_Float16)p;
+        };
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int k = 0; k < 8; ++k) take(0, k);
+        l = __builtin_fmaf(sum, back[0], l);
 #pragma unroll
-            for (int x = 0; x < kX; ++x)
-                acc[x] = mfma32(vb[i * 2 * kD + x * 32], pf[i], acc[x]);
+        for (int i = 0; i < 4; ++i) {
+            sum = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kX; ++x) {
+                const int k = i * kX + x;
+                if (k + 3 < 4 * kX) vf[(k + 3) & 3] = v_operand(buf, k + 3);
+                acc[x] = mfma32(vf[k & 3], pf[i & 1], acc[x]);
+                if (i < 3)
+#pragma unroll
+                    for (int e = x * 8 / kX; e < (x + 1) * 8 / kX; ++e) take(i + 1, e);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (i < 3) l = __builtin_fmaf(sum, back[i + 1], l);
+        }
     }
 
     if (blockIdx.x == it.base && tid == 0) a.plan[b] = make_uint2(it.base, it.splits);
     l += __shfl_xor(l, 32, kWave);
     if (!on) return;
-    const float ms = m == -kInf ? 0.0f : m, mxs = mx == -kInf ? 0.0f : mx;
-    const float norm = l == 0.0f ? 0.0f : exp2_(mxs - ms - kLift) / l;
-    const float lse2 = l == 0.0f ? -kInf : ms + __builtin_log2f(l);
-    const uint64_t prow = (uint64_t)blockIdx.x * kRowsMany + wv * 32 + col;
+    const uint64_t orow = (uint64_t)(s0 + jq) * a.heads + hq;
+    const uint64_t prow = (uint64_t)blockIdx.x * kRows + (r - row0);
+    const float norm = l == 0.0f ? 0.0f : 1.0f / l;
+    const float lse2 = l == 0.0f ? -kInf : mx - kLift + __builtin_log2f(l);
 #pragma unroll
     for (int x = 0; x < kX; ++x)
 #pragma unroll
@@ -802,12 +895,12 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
                 for (int k = 0; k < 4; ++k)
                     if (first_nan[d + k] <= limit) o[k] = __builtin_nanf("");
             }
-            if (it.splits == 1) store4<kQ>(a.out, orow + d, o);
+            if (it.splits == 1) store4<kQ>(a.out, orow * kD + d, o);
             else *reinterpret_cast<f32x4 *>(a.part + prow * kD + d) = o;
         }
     if (h == 0) {
         if (it.splits != 1) a.part_lse[prow] = lse2;
-        else if (a.lse) a.lse[orow / kD] = lse2 * 0.69314718055994531f;
+        else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
     }
 }
 
