@@ -791,6 +791,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
         for (int i = 0; i < 16; ++i) s[0][i] = s[1][i] = 0.0f;
         __builtin_amdgcn_sched_barrier(0);
         constexpr int kSteps = 2 * kK;
+        __builtin_amdgcn_s_setprio(1);              // the matrix unit before the other wave's vector work
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
             if (k + 3 < kSteps) kf[(k + 3) & 3] = k_operand(buf, k + 3);
@@ -800,6 +801,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
             for (int m = k * kOps / kSteps; m < (k + 1) * kOps / kSteps; ++m) stage(buf ^ 1, m);
             __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_s_setprio(0);
         stage_scales(t + 1, buf ^ 1);
         fetch(t + 2);
         float ks[4], ve[4], back[4];
@@ -858,6 +860,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < 8; ++k) take(0, k);
+        __builtin_amdgcn_s_setprio(1);
         l = __builtin_fmaf(sum, back[0], l);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -874,6 +877,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
             }
             if (i < 3) l = __builtin_fmaf(sum, back[i + 1], l);
         }
+        __builtin_amdgcn_s_setprio(0);
     }
 
     if (blockIdx.x == it.base && tid == 0) a.plan[b] = make_uint2(it.base, it.splits);
@@ -904,63 +908,81 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
     }
 }
 
-// Joins the splits of one output row (token, head): a workgroup's waves take
-// every fourth split each.
+// Joins the splits of 16 query rows of one key head. Groups of kD / 4 lanes take
+// a row each, or several groups a row where the rows are fewer, every group
+// some of the splits. The chunks of 16 are numbered without a scan: request b's
+// first is q_start[b] * group / 16 + b.
+constexpr uint32_t kJoinRows = 16;
+
 template <int kD, int kQ>
 __global__ __launch_bounds__(kThreads) void k_kv_join(AttendArgs few, AttendArgs many,
                                                      uint32_t tile_rows)
 {
-    constexpr int kE = kD / kWave;          // values of a lane
-    __shared__ float part[kWaves][kD];
-    __shared__ float mass[kWaves];
-    const uint32_t tokn = blockIdx.x / few.heads, h = blockIdx.x % few.heads;
-    const uint32_t b = kv_request_of(few.c.rows, tokn, [&](uint32_t r) {
+    constexpr uint32_t kLanes = kD / 4, kGroups = kThreads / kLanes;
+    __shared__ f32x4 osum[kGroups][kLanes];
+    __shared__ float wsum[kGroups];
+    const uint32_t head = blockIdx.x % few.c.kv_heads, chunk = blockIdx.x / few.c.kv_heads;
+    const uint32_t b = kv_request_of(few.c.rows, chunk, [&](uint32_t r) {
         const int32_t s = few.q_start[r];
-        return (uint64_t)(s < 0 ? 0 : s);
+        const uint64_t u = s < 0 ? 0u : ((uint32_t)s > few.total ? few.total : (uint32_t)s);
+        return u * few.group / kJoinRows + r;
     });
     uint32_t s0, s1;
     kv_span(few.q_start, b, few.total, s0, s1);
-    if (tokn < s0 || tokn >= s1) return;
-    const bool is_many = (s1 - s0) * few.group > few.most;
+    const uint32_t nrows = (s1 - s0) * few.group;
+    const int64_t r0 = ((int64_t)chunk - (int64_t)((uint64_t)s0 * few.group / kJoinRows + b)) * kJoinRows;
+    if (r0 < 0 || r0 >= nrows) return;
+    const bool is_many = nrows > few.most;
     const AttendArgs &a = is_many ? many : few;
     if (is_many) tile_rows = kRowsMany;
     const uint2 plan = a.plan[b];
     if (plan.y <= 1 || plan.y > kMaxSplits) return;
-    const uint32_t kvh = h / a.group;
-    const uint32_t r = (tokn - s0) * a.group + h % a.group;
-    const uint32_t rts = ((s1 - s0) * a.group + tile_rows - 1) / tile_rows;
-    const uint32_t first = plan.x + r / tile_rows * a.c.kv_heads + kvh, step = a.c.kv_heads * rts;
+    const uint32_t rts = (nrows + tile_rows - 1) / tile_rows;
+    const uint32_t first = plan.x + (uint32_t)r0 / tile_rows * a.c.kv_heads + head;
+    const uint32_t step = a.c.kv_heads * rts;
     if ((uint64_t)first + (uint64_t)(plan.y - 1) * step >= a.slots) return;   // q_start out of order
-    const uint64_t in = r % tile_rows;
-    float top = -kInf;
-    for (uint32_t s = lane(); s < plan.y; s += kWave)
-        top = fmaxf(top, a.part_lse[(uint64_t)(first + s * step) * tile_rows + in]);
+
+    const uint32_t rows = nrows - (uint32_t)r0 < kJoinRows ? nrows - (uint32_t)r0 : kJoinRows;
+    const uint32_t width = rows < kGroups ? rows : kGroups;       // rows at a time
+    const uint32_t share = kGroups / width;                       // groups of a row
+    const uint32_t grp = threadIdx.x / kLanes, at = threadIdx.x % kLanes;
+    const uint32_t phase = grp / width;
+    for (uint32_t base = 0; base < rows; base += width) {
+        const uint32_t row = base + grp % width;
+        const bool on = phase < share && row < rows;
+        const uint64_t in = (uint32_t)r0 % tile_rows + row;
+        float top = -kInf, w = 0.0f;
+        f32x4 o = {0, 0, 0, 0};
+        if (on) {
+            for (uint32_t s = at; s < plan.y; s += kLanes)
+                top = fmaxf(top, a.part_lse[(uint64_t)(first + s * step) * tile_rows + in]);
 #pragma unroll
-    for (int d = kWave / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-    if (top == -kInf) top = 0.0f;
-    float o[kE] = {}, w = 0.0f;
+            for (int d = (int)kLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kLanes));
+            if (top == -kInf) top = 0.0f;
 #pragma unroll 4
-    for (uint32_t s = wave(); s < plan.y; s += kWaves) {
-        const uint64_t at = (uint64_t)(first + s * step) * tile_rows + in;
-        const float v = exp2_(a.part_lse[at] - top);
-        w += v;
-#pragma unroll
-        for (int k = 0; k < kE; ++k) o[k] += v * a.part[at * kD + k * kWave + lane()];
+            for (uint32_t s = phase; s < plan.y; s += share) {
+                const uint64_t p = (uint64_t)(first + s * step) * tile_rows + in;
+                const float v = exp2_(a.part_lse[p] - top);
+                w += v;
+                o += *reinterpret_cast<const f32x4 *>(a.part + p * kD + at * 4) * v;
+            }
+        }
+        osum[grp][at] = o;
+        if (at == 0) wsum[grp] = w;
+        __syncthreads();
+        if (on && phase == 0) {
+            for (uint32_t k = 1; k < share; ++k) {
+                o += osum[grp + k * width][at];
+                w += wsum[grp + k * width];
+            }
+            const uint32_t r = (uint32_t)r0 + row;
+            const uint64_t orow = (uint64_t)(s0 + r / a.group) * a.heads + head * a.group + r % a.group;
+            store4<kQ>(a.out, orow * kD + at * 4, o * (w == 0.0f ? 0.0f : 1.0f / w));
+            if (a.lse && at == 0)
+                a.lse[orow] = w == 0.0f ? -kInf : (top + __builtin_log2f(w)) * 0.69314718055994531f;
+        }
+        __syncthreads();
     }
-#pragma unroll
-    for (int k = 0; k < kE; ++k) part[wave()][k * kWave + lane()] = o[k];
-    if (lane() == 0) mass[wave()] = w;
-    __syncthreads();
-    const float all = mass[0] + mass[1] + mass[2] + mass[3];
-    for (uint32_t d = threadIdx.x; d < kD; d += kThreads) {
-        const float v = part[0][d] + part[1][d] + part[2][d] + part[3][d];
-        const float y = all == 0.0f ? 0.0f : v / all;
-        const uint64_t at = (uint64_t)blockIdx.x * kD + d;
-        if constexpr (kQ == DMADESC_KV_BF16) static_cast<__bf16 *>(a.out)[at] = (__bf16)y;
-        else static_cast<_Float16 *>(a.out)[at] = (_Float16)y;
-    }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[blockIdx.x] = all == 0.0f ? -kInf : (top + __builtin_log2f(all)) * 0.69314718055994531f;
 }
 
 // Rows of a tile of the kernel of few rows: one product's 16 where a request's
@@ -974,7 +996,7 @@ uint32_t tile_rows_of(uint64_t total, uint32_t rows, uint32_t group)
 struct Launch {
     uint32_t tile_rows;          // of the kernel of few rows
     uint32_t few, many;          // workgroups (= partial results) of each kernel
-    bool join;
+    uint32_t join;               // workgroups of the join, 0: nothing can be split
     size_t plan_at, few_lse, few_part, many_lse, many_part, bytes;
 };
 
@@ -998,7 +1020,8 @@ Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_head
                             kv_heads * (total * group / kRowsMany +
                                         (total * group / (kMostFew + 1) < rows
                                              ? total * group / (kMostFew + 1) : rows)));
-    p.join = (p.few && split_few) || (p.many && split_many);
+    if ((p.few && split_few) || (p.many && split_many))
+        p.join = (uint32_t)(kv_heads * (total * group / kJoinRows + rows));
     size_t at = align256(8ull * rows);
     auto take = [&](size_t bytes) { const size_t r = at; at += align256(bytes); return r; };
     const size_t f = split_few ? p.few : 0, n = split_many ? p.many : 0;
@@ -1019,7 +1042,7 @@ void launch_all(const AttendArgs &few, const AttendArgs &many, const Launch &p, 
         else k_kv_attend<kD, kQ, kCodes, 2><<<p.few, kThreads, 0, s>>>(few);
     }
     if (p.join)
-        k_kv_join<kD, kQ><<<few.total * few.heads, kThreads, 0, s>>>(few, many, p.tile_rows);
+        k_kv_join<kD, kQ><<<p.join, kThreads, 0, s>>>(few, many, p.tile_rows);
 }
 
 template <int kD>
