@@ -8,6 +8,7 @@ the library cannot be loaded, importing the functions raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -158,6 +159,10 @@ def _check(func: str, rc: int) -> None:
 
 
 def _dev(t: torch.Tensor, dtype: torch.dtype, name: str, n: int | None = None) -> int:
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        have = t.numel()
+        if n is None or have == n:
+            return t.data_ptr() if have else 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.device.type != "cuda":
@@ -172,10 +177,13 @@ def _dev(t: torch.Tensor, dtype: torch.dtype, name: str, n: int | None = None) -
 
 
 def _stream(device: torch.device, stream) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    return torch._C._cuda_getCurrentRawStream(index)          # of current_stream(device)
 
 
+@functools.lru_cache(maxsize=4096)
 def workspace_bytes(op: int, n: int, param: int = 0) -> int:
     return int(lib().dmadesc_workspace_bytes(op, n, param))
 
@@ -649,6 +657,17 @@ def kv_page_bytes(kv_heads: int, page_tokens: int, dim: int) -> int:
     return int(lib().dmadesc_kv_page_bytes(kv_heads, page_tokens, dim))
 
 
+@functools.lru_cache(maxsize=4096)
+def _kv_attend_bytes(total, rows, heads, kv_heads, dim, width, page_tokens):
+    return int(lib().dmadesc_kv_attend_workspace_bytes(total, rows, heads, kv_heads, dim, width,
+                                                       page_tokens))
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv_page_bytes(kv_heads, page_tokens, dim):
+    return kv_page_bytes(kv_heads, page_tokens, dim)
+
+
 def _kv_new(size, dtype, device, stream):
     """A device tensor the call fills on `stream` (which may not be the
     current one: the allocator must not hand the memory out before it is done)."""
@@ -663,7 +682,7 @@ def _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes):
         raise ValueError("pool must be u8[npages, page_bytes] and table i32[rows, width]")
     rows, width = table.shape
     npages, nbytes = pool.shape
-    need = kv_page_bytes(kv_heads, page_tokens, dim)
+    need = _kv_page_bytes(kv_heads, page_tokens, dim)
     if need == 0 or nbytes != need:
         raise ValueError(f"a page of {kv_heads} heads x {page_tokens} tokens x {dim} values "
                          f"takes {need or 'no'} bytes, pool has {nbytes}")
@@ -674,15 +693,16 @@ def _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes):
 
 def _kv_rows(t, name, total, heads, dim, types):
     """(pointer, token stride, head stride) of a [total, heads, dim] operand."""
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor, got {t.device}")
     if t.dtype not in types:
         raise TypeError(f"{name}: {t.dtype} is not taken")
     if t.shape != (total, heads, dim):
         raise ValueError(f"{name}: expected shape {(total, heads, dim)}, got {tuple(t.shape)}")
-    if t.stride(2) != 1:
+    tok, head, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), tok, head
 
 
 def _kv_refused(func: str, status: torch.Tensor, stream, out: dict) -> None:
@@ -749,10 +769,10 @@ def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table:
     if out is None:
         out = dict(out=_kv_new((total, heads, dim), q.dtype, dev, stream),
                    lse=_kv_new((total, heads), torch.float32, dev, stream))
-    need = lib().dmadesc_kv_attend_workspace_bytes(total, cache.rows, heads, kv_heads, dim,
-                                                   cache.width, page_tokens)
     if ws is None:
-        ws = _kv_new(need, torch.uint8, dev, stream)
+        rows, width = table.shape
+        ws = _kv_new(_kv_attend_bytes(total, rows, heads, kv_heads, dim, width, page_tokens),
+                     torch.uint8, dev, stream)
     rc = lib().dmadesc_kv_attend(
         ctypes.byref(cache), *qp, qs, total, heads, _KV_TYPE[q.dtype],
         KV_CAUSAL if causal else 0, 0.0 if scale is None else scale,

@@ -31,13 +31,17 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 64;                   // tokens a wave handles at a time
-// Workgroups that a call's work is cut into, and the least tiles of a part:
-// for the kernel of few rows and for that of many.
-constexpr uint32_t kTargetFew = 1024, kMinTilesFew = 16;
-constexpr uint32_t kTargetMany = 512, kMinTilesMany = 4;
+// Workgroups of each kernel that fit the 256 compute units at once.
+constexpr int few_occupancy(int dim, int nt)   // waves a SIMD, by the registers of the accumulators
+{
+    return dim * nt <= 64 ? 3 : dim * nt <= 128 ? 2 : 1;
+}
+constexpr uint32_t slots_few(int dim, int nt) { return 512u * few_occupancy(dim, nt); }
+constexpr uint32_t slots_many(int dim) { return dim == 64 ? 768 : dim == 128 ? 512 : 256; }
+constexpr uint32_t kWholeFew = 32, kWholeMany = 8;      // tiles up to which nothing is split
 constexpr uint32_t kMaxSplits = 256;
 constexpr uint32_t kRowsMany = 128;         // query rows of a workgroup of the kernel of many
-constexpr uint32_t kMostFew = 64;           // query rows per key head up to which rows are few
+constexpr uint32_t kMostFew = 64;           // rows up to which a request is the first's, if both run
 constexpr float kShift = 15.0f;             // probabilities are at most 2^15 in f16
 
 struct AttendArgs {
@@ -58,9 +62,11 @@ struct AttendArgs {
 };
 
 // One piece of work: the split-th of `splits` even parts of the cache that one
-// row tile of one key head of request b sees.
+// row tile of one key head of request b sees. The request's new tokens are
+// s0 .. s0 + news - 1, its length is len.
 struct Item {
-    uint32_t b, split, splits, head, rt, base;
+    uint32_t b, split, splits, head, rt, base, s0;
+    int news, len;
 };
 
 template <int kQ> struct QFrag;
@@ -116,82 +122,157 @@ __device__ __forceinline__ V8 codes8(uint32_t lo, uint32_t hi)
     return V8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Row tiles and cache tiles of request b; no row tiles if it is not this
-// kernel's.
-template <int kRows>
-__device__ __forceinline__ void request_size(const AttendArgs &a, uint32_t b, uint32_t &rts,
-                                             uint32_t &tiles)
-{
-    uint32_t s0, s1;
-    kv_span(a.q_start, b, a.total, s0, s1);
-    const uint32_t n = (s1 - s0) * a.group;             // total * heads < 2^31
-    rts = n < a.least || n > a.most ? 0u : (n + kRows - 1) / kRows;
-    tiles = ((uint32_t)kv_len(a.c, b) + kTile - 1) / kTile;
-}
+// What a call's requests are cut into: about as many pieces as workgroups fit
+// the card at once (kSlots), so that they run in one round of equal pieces, but
+// no piece below kLeast tiles, and nothing where no request has more than kWhole:
+// the join costs 5 us, what a wave needs for about eight tiles. The
+// host knows only bounds, so every workgroup adds the lengths up for itself and
+// finds its own piece, which costs less than a launch that would do it once:
+// up to 64 requests are one load and a few lane exchanges of each wave.
+template <int kRows, int kThreads, uint32_t kSlots, uint32_t kLeast, uint32_t kWhole>
+struct Plan {
+    static constexpr int kWaves = kThreads / kWave;
 
-__device__ __forceinline__ uint32_t splits_of(uint32_t tiles, uint32_t chunk)
-{
-    const uint32_t s = (tiles + chunk - 1) / chunk;
-    return s < 1 ? 1u : (s > kMaxSplits ? kMaxSplits : s);
-}
+    struct Size {
+        uint32_t rts, tiles, s0;      // row tiles (0: not this kernel's request), cache tiles
+        int news, len;
+    };
 
-// The item of workgroup `id`, from the requests' lengths on the device (the
-// host knows only bounds): the tiles of all requests are cut into about
-// kTarget pieces of equal size. Every workgroup adds the lengths up for
-// itself, one round for up to 256 requests, which costs less than a launch
-// that would do it once. Returns false for workgroups past the last item.
-template <int kRows, uint32_t kTarget, uint32_t kMinTiles>
-__device__ bool find_item(const AttendArgs &a, uint32_t id, Item &it)
-{
-    __shared__ uint64_t sums[kWaves];
-    __shared__ uint32_t scan[kWaves];
-    __shared__ Item found;
-    __shared__ uint32_t hit;
-    const uint32_t rows = a.c.rows, heads = a.c.kv_heads;
-    uint64_t work = 0;
-    for (uint32_t b = threadIdx.x; b < rows; b += kThreads) {
-        uint32_t rts, tiles;
-        request_size<kRows>(a, b, rts, tiles);
-        work += (uint64_t)rts * tiles;
+    static __device__ __forceinline__ Size size(const AttendArgs &a, uint32_t b)
+    {
+        Size z{};
+        if (b >= a.c.rows) return z;
+        uint32_t s1;
+        kv_span(a.q_start, b, a.total, z.s0, s1);
+        z.news = (int)(s1 - z.s0);
+        z.len = kv_len(a.c, b);
+        const uint32_t n = (uint32_t)z.news * a.group;      // total * heads < 2^31
+        z.rts = n < a.least || n > a.most ? 0u : (n + kRows - 1) / kRows;
+        z.tiles = ((uint32_t)z.len + kTile - 1) / kTile;
+        return z;
     }
-    work = wave_sum(work);
-    if (lane() == 0) sums[wave()] = work;
-    if (threadIdx.x == 0) hit = 0;
-    __syncthreads();
-    work = 0;
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) work += sums[k];
-    const uint64_t even = (work * heads + kTarget - 1) / kTarget;
-    const uint32_t chunk = even < kMinTiles ? kMinTiles : (uint32_t)even;
 
-    uint64_t run = 0;
-    for (uint32_t b0 = 0; b0 < rows; b0 += kThreads) {
-        const uint32_t b = b0 + threadIdx.x;
-        uint32_t rts = 0, tiles = 0, splits = 0;
-        if (b < rows) {
-            request_size<kRows>(a, b, rts, tiles);
-            splits = splits_of(tiles, chunk);
+    static __device__ __forceinline__ uint32_t splits(const Size &z, uint32_t chunk)
+    {
+        const uint32_t s = (z.tiles + chunk - 1) / chunk;
+        return s < 1 ? 1u : (s > kMaxSplits ? kMaxSplits : s);
+    }
+
+    // Tiles of a piece for `work` tiles in `base` unsplit pieces: a request's last
+    // piece is half full on the average.
+    static __device__ __forceinline__ uint32_t first_chunk(float work, float base, bool whole)
+    {
+        if (whole) return kWhole;
+        const float room = fmaxf((float)kSlots - 0.5f * base, 0.25f * kSlots);
+        const float c = ceilf(work / room);
+        return c < (float)kLeast ? kLeast : (uint32_t)c;
+    }
+
+    static __device__ __forceinline__ bool fits(uint32_t pieces, float base)
+    {
+        return pieces <= kSlots || base >= (float)kSlots;
+    }
+
+    static __device__ __forceinline__ uint32_t larger(uint32_t chunk) { return chunk + chunk / 16 + 1; }
+
+    static __device__ __forceinline__ Item item(const Size &z, uint32_t b, uint32_t at, uint32_t k,
+                                                uint32_t parts, uint32_t heads)
+    {
+        // Heads first: workgroups go round the 8 XCDs, so a head's meet in few caches.
+        return Item{b, k / heads / z.rts, parts, k % heads, k / heads % z.rts, at, z.s0, z.news, z.len};
+    }
+
+    // The piece of workgroup `id`; false past the last. Every wave of the
+    // workgroup calls it (with more than 64 requests it has barriers).
+    static __device__ bool find(const AttendArgs &a, uint32_t id, Item &it)
+    {
+        const uint32_t rows = a.c.rows, heads = a.c.kv_heads;
+        if (rows <= (uint32_t)kWave) {
+            const Size z = size(a, (uint32_t)lane());
+            const float work = wave_sum((float)z.rts * (float)z.tiles) * (float)heads;
+            const float base = wave_sum((float)z.rts) * (float)heads;
+            uint32_t chunk = first_chunk(work, base, __ballot(z.rts > 0 && z.tiles > kWhole) == 0);
+            uint32_t mine = z.rts * splits(z, chunk) * heads, upto = wave_incl_scan(mine);
+            for (int k = 0; k < 4 && !fits(__builtin_amdgcn_readlane(upto, kWave - 1), base); ++k) {
+                chunk = larger(chunk);
+                mine = z.rts * splits(z, chunk) * heads;
+                upto = wave_incl_scan(mine);
+            }
+            const uint64_t hit = __ballot(id < upto && id >= upto - mine);
+            if (hit == 0) return false;
+            const int b = __ffsll((unsigned long long)hit) - 1;
+            const auto get = [b](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, b); };
+            const Size w{get(z.rts), get(z.tiles), get(z.s0), (int)get((uint32_t)z.news),
+                         (int)get((uint32_t)z.len)};
+            const uint32_t at = get(upto - mine);
+            it = item(w, (uint32_t)b, at, id - at, splits(w, chunk), heads);
+            return true;
         }
-        const uint32_t mine = rts * splits * heads;
-        uint32_t all;
-        const uint64_t at = run + block_excl_scan<kThreads, uint32_t>(mine, scan, &all);
-        if (id >= at && id < at + mine) {
-            const uint32_t k = id - (uint32_t)at;
-            found.b = b;
-            found.head = k % heads;        // workgroups go round the 8 XCDs: a head's on few of them
-            found.rt = k / heads % rts;
-            found.split = k / heads / rts;
-            found.splits = splits;
-            found.base = (uint32_t)at;
-            hit = 1;
+        __shared__ float fsum[2][kWaves];
+        __shared__ uint32_t scan[kWaves];
+        __shared__ Item found;
+        __shared__ uint32_t hit, large;
+        if (threadIdx.x == 0) hit = large = 0;
+        __syncthreads();
+        float work = 0.0f, base = 0.0f;
+        for (uint32_t b = threadIdx.x; b < rows; b += kThreads) {
+            const Size z = size(a, b);
+            work += (float)z.rts * (float)z.tiles;
+            base += (float)z.rts;
+            if (z.rts > 0 && z.tiles > kWhole) large = 1;         // every writer writes 1
+        }
+        work = wave_sum(work);
+        base = wave_sum(base);
+        if (lane() == 0) {
+            fsum[0][wave()] = work;
+            fsum[1][wave()] = base;
         }
         __syncthreads();
-        run += all;
-        if (hit || run > id) break;
+        work = base = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) {
+            work += fsum[0][k];
+            base += fsum[1][k];
+        }
+        work *= (float)heads;
+        base *= (float)heads;
+        uint32_t chunk = first_chunk(work, base, large == 0);
+        for (int k = 0; k < 4; ++k) {
+            uint32_t n = 0;
+            for (uint32_t b = threadIdx.x; b < rows; b += kThreads) {
+                const Size z = size(a, b);
+                n += z.rts * splits(z, chunk) * heads;
+            }
+            n = wave_sum(n);
+            __syncthreads();
+            if (lane() == 0) scan[wave()] = n;
+            __syncthreads();
+            n = 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) n += scan[w];
+            if (fits(n, base)) break;
+            chunk = larger(chunk);
+        }
+        uint64_t run = 0;
+        for (uint32_t b0 = 0; b0 < rows; b0 += kThreads) {
+            const uint32_t b = b0 + threadIdx.x;
+            const Size z = size(a, b);
+            const uint32_t parts = splits(z, chunk), mine = z.rts * parts * heads;
+            uint32_t all;
+            __syncthreads();
+            const uint64_t at = run + block_excl_scan<kThreads, uint32_t>(mine, scan, &all);
+            if (id >= at && id < at + mine) {
+                found = item(z, b, (uint32_t)at, id - (uint32_t)at, parts, heads);
+                hit = 1;
+            }
+            __syncthreads();
+            run += all;
+            if (hit || run > id) break;
+        }
+        it = found;
+        return hit != 0;
     }
-    it = found;
-    return hit != 0;
-}
+};
 
 template <int kQ>
 __device__ __forceinline__ void store4(void *out, uint64_t at, f32x4 v)
@@ -245,29 +326,29 @@ constexpr float kInf = __builtin_inff();
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 template <int kD, int kQ, int kCodes, int kNt>
-__global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(AttendArgs a)
+__global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(AttendArgs a)
 {
     constexpr int kRows = 16 * kNt;
     constexpr int kC = kD / 64;             // 64-dimension pieces of a key row
     constexpr int kX = kD / 16;             // 16-dimension pieces of the output
     typedef typename QFrag<kQ>::type Q8;
-    __shared__ f32x4 obuf[2][kX][kWave];
+    __shared__ f32x4 obuf[kWaves][kX][kWave];
     __shared__ float stat[3][kWaves][kRows];
     __shared__ int first_nan[kD];
 
     Item it;
+    if (!Plan<kRows, kThreads, slots_few(kD, kNt), 8, kWholeFew>::find(a, blockIdx.x, it)) return;
     for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
-    if (!find_item<kRows, kTargetFew, kMinTilesFew>(a, blockIdx.x, it)) return;   // has barriers
+    __syncthreads();
     const KvView &c = a.c;
     const int ln = lane(), col = ln & 15, g = ln >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(wave());
     const uint32_t b = __builtin_amdgcn_readfirstlane(it.b);
     const uint32_t head = __builtin_amdgcn_readfirstlane(it.head);
-    const uint32_t row0 = __builtin_amdgcn_readfirstlane(it.rt) * kRows;
-    uint32_t s0, s1;
-    kv_span(a.q_start, b, a.total, s0, s1);
-    const int len = kv_len(c, b), news = (int)(s1 - s0);
+    const uint32_t s0 = __builtin_amdgcn_readfirstlane(it.s0);
+    const int len = __builtin_amdgcn_readfirstlane(it.len), news = __builtin_amdgcn_readfirstlane(it.news);
     const uint32_t nrows = (uint32_t)news * a.group;
+    const uint32_t row0 = __builtin_amdgcn_readfirstlane(it.rt) * kRows;
     const int per = (int)c.tshift - 4;
     const uint32_t sub_mask = (1u << per) - 1u;
 
@@ -275,26 +356,18 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
     Q8 qf[kNt][kC][2];
     int limit[kNt];
     uint64_t orow[kNt];
-    int low = len - 1, high = -1;           // least and largest limit of the tile's rows
-    {
-        const uint32_t jl = row0 / a.group;
+    int low = len - 1, high = len - 1;      // least and largest limit of the tile's rows
+    if (a.causal) {
         const uint32_t last = nrows - 1 < row0 + kRows - 1 ? nrows - 1 : row0 + kRows - 1;
-        if (a.causal) {
-            low = len - news + (int)jl;
-            high = len - news + (int)(last / a.group);
-        } else {
-            high = len - 1;
-        }
-        low = low < len - 1 ? low : len - 1;
-        high = high < len - 1 ? high : len - 1;
+        low = len - news + (int)(row0 / a.group);
+        high = len - news + (int)(last / a.group);
     }
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
         const uint32_t r = row0 + n * 16 + col;
         const bool on = r < nrows;
         const uint32_t rr = on ? r : 0u, j = rr / a.group, h = head * a.group + rr % a.group;
-        const int lim = a.causal ? len - news + (int)j : len - 1;
-        limit[n] = on ? (lim < len - 1 ? lim : len - 1) : -1;
+        limit[n] = !on ? -1 : a.causal ? len - news + (int)j : len - 1;
         orow[n] = ((uint64_t)(s0 + j) * a.heads + h) * kD;
         const uint16_t *const q = static_cast<const uint16_t *>(a.q) +
                                   (int64_t)(s0 + j) * a.q_tok + (int64_t)h * a.q_head + 16 * g;
@@ -370,10 +443,14 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
         load_pages(t);
         load_k(t);
         load_v(t);
-        load_pages(t + kWaves);
+        load_pages(t + kWaves < t1 ? t + kWaves : t);
     }
+    // The loads of the wave's next tile are in flight under the products of this
+    // one. They are made in the last round too, of that tile again: were they
+    // conditional, the wait for K at the top would have to be one for all loads.
     for (; t < t1; t += kWaves) {
-        const bool more = t + kWaves < t1;
+        const int after = t + kWaves < t1 ? t + kWaves : t;
+        const int later = t + 2 * kWaves < t1 ? t + 2 * kWaves : after;
         f32x4 s[kNt][4];
 #pragma unroll
         for (int n = 0; n < kNt; ++n)
@@ -391,7 +468,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
                 }
         const float kscale = ks * a.scale, vscale = vs;
         const int nvalid = valid;
-        if (more) load_k(t + kWaves);
+        load_k(after);
 
         const int tok = t * kTile + g * kBlock;       // first token of the lane's block
         const bool edge = t * kTile + kTile - 1 > low;   // some row does not see the whole tile
@@ -462,13 +539,12 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
 #pragma unroll
                 for (int n = 0; n < kNt; ++n) acc[n][x] = mfma(vf, pf[n][u], acc[n][x]);
             }
-        if (more) {
-            load_v(t + kWaves);
-            load_pages(t + 2 * kWaves);
-        }
+        load_v(after);
+        load_pages(later);
     }
 
-    // Join the waves: common maxima first, then the sums, two waves at a time.
+    // Join the waves: common references first, then the sums through LDS, each
+    // wave adding up its share of the 16-dimension pieces.
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
         l[n] += __shfl_xor(l[n], 16, kWave);
@@ -479,10 +555,9 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
             stat[2][wv][n * 16 + col] = l[n];
         }
     }
+    if (blockIdx.x == it.base && threadIdx.x == 0) a.plan[b] = make_uint2(it.base, it.splits);
     __syncthreads();
     const bool whole = it.splits == 1;
-    const uint32_t slot = blockIdx.x;       // the item's number is its partial result's
-    if (slot == it.base && threadIdx.x == 0) a.plan[b] = make_uint2(it.base, it.splits);
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
         float ma = -kInf, mxa = -kInf, la = 0.0f;
@@ -496,47 +571,33 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend(Atten
         for (int w = 0; w < kWaves; ++w)
             la += stat[2][w][n * 16 + col] * exp2_(stat[0][w][n * 16 + col] - ms);
         const float mine = exp2_(mx[n] - mxs);
+        if (n > 0) __syncthreads();                 // the sums of n - 1 are read
 #pragma unroll
-        for (int x = 0; x < kX; ++x) acc[n][x] *= mine;
-        if (wv >= 2)
-#pragma unroll
-            for (int x = 0; x < kX; ++x) obuf[wv - 2][x][ln] = acc[n][x];
+        for (int x = 0; x < kX; ++x) obuf[wv][x][ln] = acc[n][x] * mine;
         __syncthreads();
-        if (wv < 2)
+        // A row that sees nothing: zero, and no mass (la = 0).
+        const float norm = la == 0.0f ? 0.0f : exp2_(mxs - ms - kShift) / la;
+        const float lse2 = la == 0.0f ? -kInf : ms + __builtin_log2f(la);
+        const uint64_t prow = (uint64_t)blockIdx.x * kRows + n * 16 + col;   // of the partial results
+        if (row0 + n * 16 + col < nrows) {
+            for (int x = wv; x < kX; x += kWaves) {
+                f32x4 o = obuf[0][x][ln];
 #pragma unroll
-            for (int x = 0; x < kX; ++x) acc[n][x] += obuf[wv][x][ln];
-        __syncthreads();
-        if (wv == 1)
+                for (int w = 1; w < kWaves; ++w) o += obuf[w][x][ln];
+                o *= norm;
+                if (kCodes == DMADESC_KV_E4M3) {
 #pragma unroll
-            for (int x = 0; x < kX; ++x) obuf[0][x][ln] = acc[n][x];
-        __syncthreads();
-        if (wv == 0) {
-            const uint32_t r = row0 + n * 16 + col;
-            // A row that sees nothing: zero, and no mass (la = 0).
-            const float norm = la == 0.0f ? 0.0f : exp2_(mxs - ms - kShift) / la;
-            const float lse2 = la == 0.0f ? -kInf : ms + __builtin_log2f(la);
-            if (r < nrows) {
-#pragma unroll
-                for (int x = 0; x < kX; ++x) {
-                    f32x4 o = (acc[n][x] + obuf[0][x][ln]) * norm;
-                    if (kCodes == DMADESC_KV_E4M3) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (first_nan[16 * x + 4 * g + i] <= limit[n]) o[i] = __builtin_nanf("");
-                    }
-                    if (whole)
-                        store4<kQ>(a.out, orow[n] + 16 * x + 4 * g, o);
-                    else
-                        *reinterpret_cast<f32x4 *>(
-                            a.part + ((uint64_t)slot * kRows + n * 16 + col) * kD + 16 * x + 4 * g) = o;
+                    for (int i = 0; i < 4; ++i)
+                        if (first_nan[16 * x + 4 * g + i] <= limit[n]) o[i] = __builtin_nanf("");
                 }
-                if (g == 0) {
-                    if (!whole) a.part_lse[(uint64_t)slot * kRows + n * 16 + col] = lse2;
-                    else if (a.lse) a.lse[orow[n] / kD] = lse2 * 0.69314718055994531f;
-                }
+                if (whole) store4<kQ>(a.out, orow[n] + 16 * x + 4 * g, o);
+                else *reinterpret_cast<f32x4 *>(a.part + prow * kD + 16 * x + 4 * g) = o;
+            }
+            if (wv == 0 && g == 0) {
+                if (!whole) a.part_lse[prow] = lse2;
+                else if (a.lse) a.lse[orow[n] / kD] = lse2 * 0.69314718055994531f;
             }
         }
-        __syncthreads();
     }
 }
 
@@ -580,7 +641,7 @@ __device__ __forceinline__ float half_max(float x)
 // tile's exponentials are taken, and the next codes converted under the product
 // with V.
 template <int kD, int kQ, int kCodes>
-__global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(AttendArgs a)
+__global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_kv_attend_many(AttendArgs a)
 {
     constexpr int kK = kD / 16;                     // steps of the first product
     constexpr int kX = kD / 32;                     // 32-dimension pieces of the output
@@ -596,8 +657,9 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
     __shared__ int first_nan[kD];
 
     Item it;
+    if (!Plan<kRows, kThreads, slots_many(kD), 4, kWholeMany>::find(a, blockIdx.x, it)) return;
     for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
-    if (!find_item<kRows, kTargetMany, kMinTilesMany>(a, blockIdx.x, it)) return;   // has barriers
+    __syncthreads();
     const KvView &c = a.c;
     const int ln = lane(), col = ln & 31, h = ln >> 5, tid = (int)threadIdx.x;
     const int wv = __builtin_amdgcn_readfirstlane(wave());
@@ -605,9 +667,8 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_kv_attend_many(
     const uint32_t head = __builtin_amdgcn_readfirstlane(it.head);
     const uint32_t row0 = __builtin_amdgcn_readfirstlane(it.rt) * kRows;
     const uint32_t wrow0 = row0 + wv * 32;   // first row of the wave
-    uint32_t s0, s1;
-    kv_span(a.q_start, b, a.total, s0, s1);
-    const int len = kv_len(c, b), news = (int)(s1 - s0);
+    const uint32_t s0 = __builtin_amdgcn_readfirstlane(it.s0);
+    const int len = __builtin_amdgcn_readfirstlane(it.len), news = __builtin_amdgcn_readfirstlane(it.news);
     const uint32_t nrows = (uint32_t)news * a.group;
     const int per = (int)c.tshift - 4;
     const uint32_t sub_mask = (1u << per) - 1u;
@@ -985,17 +1046,18 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(AttendArgs few, AttendArgs
     }
 }
 
-// Rows of a tile of the kernel of few rows: one product's 16 where a request's
-// rows fit it, else 32.
-uint32_t tile_rows_of(uint64_t total, uint32_t rows, uint32_t group)
-{
-    return (total + rows - 1) / rows * group <= 16 ? 16u : 32u;
-}
-
-// How a call's memory and launches follow from what the host knows.
+// How a call's memory and launches follow from what the host knows, which is
+// not the requests' own sizes. Where a request has more than 32 query rows per
+// key head on the average, the kernel of many rows takes them all (its reads of
+// the cache are as good as the other's); otherwise the kernel of few rows does.
+// Only where some request may have more than 256 rows beside those few, a chunk
+// of a prompt among single tokens, are both launched and share the requests: an
+// idle launch costs 5 us, and a request of up to 256 rows as much as that in the
+// wrong kernel.
 struct Launch {
-    uint32_t tile_rows;          // of the kernel of few rows
+    uint32_t tile_rows;          // of the kernel of few rows: one product's 16, or 32
     uint32_t few, many;          // workgroups (= partial results) of each kernel
+    uint32_t most;               // rows of a request up to which it is the first kernel's
     uint32_t join;               // workgroups of the join, 0: nothing can be split
     size_t plan_at, few_lse, few_part, many_lse, many_part, bytes;
 };
@@ -1004,24 +1066,24 @@ Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_head
                  uint64_t tokens)
 {
     Launch p{};
-    const uint32_t group = heads / kv_heads;
-    p.tile_rows = tile_rows_of(total, rows, group);
-    // The even pieces, and one more for each row tile of each key head. A
-    // request's rows are many only if all rows together are; a call's only
-    // request has all of them.
-    const bool many = total * group > kMostFew;
-    const uint64_t most = (tokens + kTile - 1) / kTile;
-    const bool split_few = most > kMinTilesFew, split_many = most > kMinTilesMany;
-    if (!(many && rows == 1))
-        p.few = (uint32_t)((split_few ? kTargetFew : 0u) +
-                           kv_heads * (total * group / p.tile_rows + rows));
-    if (many)
-        p.many = (uint32_t)((split_many ? kTargetMany : 0u) +
-                            kv_heads * (total * group / kRowsMany +
-                                        (total * group / (kMostFew + 1) < rows
-                                             ? total * group / (kMostFew + 1) : rows)));
+    const uint64_t group = heads / kv_heads, all = total * group;
+    const uint64_t mean = (total + rows - 1) / rows * group;
+    const uint64_t tiles = (tokens + kTile - 1) / kTile;
+    const bool split_few = tiles > kWholeFew, split_many = tiles > kWholeMany;
+    const bool few = mean <= 48, both = few && total > rows && (total - rows) * group > 256;
+    p.most = !few ? 0u : both ? kMostFew : ~0u;
+    p.tile_rows = mean <= 16 ? 16u : mean <= 32 ? 32u : 48u;
+    // The even pieces, and one more for each row tile of each key head: at most
+    // all rows' whole tiles and one of each request.
+    const uint64_t few_rows = both && all > rows * (uint64_t)kMostFew ? rows * (uint64_t)kMostFew : all;
+    const uint64_t big = both ? all / (kMostFew + 1) : rows;      // requests that have many
+    if (few)
+        p.few = (uint32_t)((split_few ? slots_few((int)dim, (int)p.tile_rows / 16) : 0u) + kv_heads * (few_rows / p.tile_rows + rows));
+    if (!few || both)
+        p.many = (uint32_t)((split_many ? slots_many((int)dim) : 0u) +
+                            kv_heads * (all / kRowsMany + (big < rows ? big : rows)));
     if ((p.few && split_few) || (p.many && split_many))
-        p.join = (uint32_t)(kv_heads * (total * group / kJoinRows + rows));
+        p.join = (uint32_t)(kv_heads * (all / kJoinRows + rows));
     size_t at = align256(8ull * rows);
     auto take = [&](size_t bytes) { const size_t r = at; at += align256(bytes); return r; };
     const size_t f = split_few ? p.few : 0, n = split_many ? p.many : 0;
@@ -1039,7 +1101,8 @@ void launch_all(const AttendArgs &few, const AttendArgs &many, const Launch &p, 
     if (p.many) k_kv_attend_many<kD, kQ, kCodes><<<p.many, kThreads, 0, s>>>(many);
     if (p.few) {
         if (p.tile_rows == 16) k_kv_attend<kD, kQ, kCodes, 1><<<p.few, kThreads, 0, s>>>(few);
-        else k_kv_attend<kD, kQ, kCodes, 2><<<p.few, kThreads, 0, s>>>(few);
+        else if (p.tile_rows == 32) k_kv_attend<kD, kQ, kCodes, 2><<<p.few, kThreads, 0, s>>>(few);
+        else k_kv_attend<kD, kQ, kCodes, 3><<<p.few, kThreads, 0, s>>>(few);
     }
     if (p.join)
         k_kv_join<kD, kQ><<<p.join, kThreads, 0, s>>>(few, many, p.tile_rows);
@@ -1095,11 +1158,11 @@ hipError_t launch_kv_attend(const KvAttendArgs &k, hipStream_t s)
     few.part_lse = reinterpret_cast<float *>(ws + p.few_lse);
     few.slots = p.few;
     few.least = 1;
-    few.most = kMostFew;
+    few.most = p.most;
     many.part = reinterpret_cast<float *>(ws + p.many_part);
     many.part_lse = reinterpret_cast<float *>(ws + p.many_lse);
     many.slots = p.many;
-    many.least = kMostFew + 1;
+    many.least = p.most + 1;
     many.most = ~0u;
     if (c.dim == 64) launch_dim<64>(k, few, many, p, s);
     else if (c.dim == 128) launch_dim<128>(k, few, many, p, s);
