@@ -441,106 +441,110 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
     int t = t0 + wv;
     if (t < t1) {
         load_pages(t);
+        // Wait for the queries here, with the pages: left to their first use, the
+        // wait would stand in the loop and be one for all loads.
+        __builtin_amdgcn_s_waitcnt(0x0f70);         // vmcnt(0)
         load_k(t);
         load_v(t);
         load_pages(t + kWaves < t1 ? t + kWaves : t);
-    }
-    // The loads of the wave's next tile are in flight under the products of this
-    // one. They are made in the last round too, of that tile again: were they
-    // conditional, the wait for K at the top would have to be one for all loads.
-    for (; t < t1; t += kWaves) {
-        const int after = t + kWaves < t1 ? t + kWaves : t;
-        const int later = t + 2 * kWaves < t1 ? t + 2 * kWaves : after;
-        f32x4 s[kNt][4];
+        // The loads of the wave's next tile are in flight under the products of this
+        // one. They are made in the last round too, of that tile again: were they
+        // conditional, the wait for K at the top would have to be one for all loads.
+        do {
+            const int after = t + kWaves < t1 ? t + kWaves : t;
+            const int later = t + 2 * kWaves < t1 ? t + 2 * kWaves : after;
+            f32x4 s[kNt][4];
 #pragma unroll
-        for (int n = 0; n < kNt; ++n)
+            for (int n = 0; n < kNt; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[n][j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int k = 0; k < kC; ++k)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const Q8 kf = codes8<kCodes, Q8>(kr[j][k][2 * u], kr[j][k][2 * u + 1]);
-#pragma unroll
-                    for (int n = 0; n < kNt; ++n) s[n][j] = mfma(kf, qf[n][k][u], s[n][j]);
-                }
-        const float kscale = ks * a.scale, vscale = vs;
-        const int nvalid = valid;
-        load_k(after);
-
-        const int tok = t * kTile + g * kBlock;       // first token of the lane's block
-        const bool edge = t * kTile + kTile - 1 > low;   // some row does not see the whole tile
-        const float ve = (float)((int)(__float_as_uint(vscale) >> 23 & 0xffu) - 126);
-        f16x8 pf[kNt][2];
-#pragma unroll
-        for (int n = 0; n < kNt; ++n) {
-            const int lim = nvalid == 0 ? -1 : limit[n];
-            float top = -kInf;
+                for (int j = 0; j < 4; ++j) s[n][j] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float v = s[n][j][i] * kscale;
-                    s[n][j][i] = tok + 4 * j + i <= lim ? v : -kInf;
-                    top = fmaxf(top, s[n][j][i]);
-                }
-            float topv = top == -kInf ? -kInf : top + ve;
-            top = fmaxf(top, __shfl_xor(top, 16, kWave));
-            topv = fmaxf(topv, __shfl_xor(topv, 16, kWave));
-            top = fmaxf(top, __shfl_xor(top, 32, kWave));
-            topv = fmaxf(topv, __shfl_xor(topv, 32, kWave));
-            const float mn = fmaxf(m[n], top), mxn = fmaxf(mx[n], topv);
-            const float ms = mn == -kInf ? 0.0f : mn, mxs = mxn == -kInf ? 0.0f : mxn;
-            const float f = nvalid == 0 ? 0.0f : vscale * exp2_(ms - mxs + kShift);
-            float sum = 0.0f;
+                for (int k = 0; k < kC; ++k)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                    for (int u = 0; u < 2; ++u) {
+                        const Q8 kf = codes8<kCodes, Q8>(kr[j][k][2 * u], kr[j][k][2 * u + 1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p = exp2_(s[n][j][i] - ms);
-                    sum += p;
-                    pf[n][j >> 1][(j & 1) * 4 + i] = (_Float16)(p * f);
-                }
-            l[n] = l[n] * exp2_(m[n] - ms) + sum;
-            const float back = exp2_(mx[n] - mxs);
-            m[n] = mn;
-            mx[n] = mxn;
-#pragma unroll
-            for (int x = 0; x < kX; ++x) acc[n][x] *= back;
-        }
+                        for (int n = 0; n < kNt; ++n) s[n][j] = mfma(kf, qf[n][k][u], s[n][j]);
+                    }
+            const float kscale = ks * a.scale, vscale = vs;
+            const int nvalid = valid;
+            load_k(after);
 
-        if (kCodes == DMADESC_KV_E4M3 && edge) {
-            uint32_t found = 0;
+            const int tok = t * kTile + g * kBlock;       // first token of the lane's block
+            const bool edge = t * kTile + kTile - 1 > low;   // some row does not see the whole tile
+            const float ve = (float)((int)(__float_as_uint(vscale) >> 23 & 0xffu) - 126);
+            f16x8 pf[kNt][2];
 #pragma unroll
-            for (int x = 0; x < kX; ++x)
+            for (int n = 0; n < kNt; ++n) {
+                const int lim = nvalid == 0 ? -1 : limit[n];
+                float top = -kInf;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    vr[x][q] &= keep_mask(nvalid, q);
-                    found |= nan_bytes(vr[x][q]);
-                }
-            if (__ballot(found != 0)) {
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = s[n][j][i] * kscale;
+                        s[n][j][i] = tok + 4 * j + i <= lim ? v : -kInf;
+                        top = fmaxf(top, s[n][j][i]);
+                    }
+                float topv = top == -kInf ? -kInf : top + ve;
+                top = fmaxf(top, __shfl_xor(top, 16, kWave));
+                topv = fmaxf(topv, __shfl_xor(topv, 16, kWave));
+                top = fmaxf(top, __shfl_xor(top, 32, kWave));
+                topv = fmaxf(topv, __shfl_xor(topv, 32, kWave));
+                const float mn = fmaxf(m[n], top), mxn = fmaxf(mx[n], topv);
+                const float ms = mn == -kInf ? 0.0f : mn, mxs = mxn == -kInf ? 0.0f : mxn;
+                const float f = nvalid == 0 ? 0.0f : vscale * exp2_(ms - mxs + kShift);
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p = exp2_(s[n][j][i] - ms);
+                        sum += p;
+                        pf[n][j >> 1][(j & 1) * 4 + i] = (_Float16)(p * f);
+                    }
+                l[n] = l[n] * exp2_(m[n] - ms) + sum;
+                const float back = exp2_(mx[n] - mxs);
+                m[n] = mn;
+                mx[n] = mxn;
+#pragma unroll
+                for (int x = 0; x < kX; ++x) acc[n][x] *= back;
+            }
+
+            if (kCodes == DMADESC_KV_E4M3 && edge) {
+                uint32_t found = 0;
 #pragma unroll
                 for (int x = 0; x < kX; ++x)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t z = nan_bytes(vr[x][q]);
-                        note_nan(first_nan, z, 16 * x + col, tok + 4 * q);
-                        vr[x][q] = without(vr[x][q], z);
+                        vr[x][q] &= keep_mask(nvalid, q);
+                        found |= nan_bytes(vr[x][q]);
                     }
+                if (__ballot(found != 0)) {
+#pragma unroll
+                    for (int x = 0; x < kX; ++x)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t z = nan_bytes(vr[x][q]);
+                            note_nan(first_nan, z, 16 * x + col, tok + 4 * q);
+                            vr[x][q] = without(vr[x][q], z);
+                        }
+                }
             }
-        }
 #pragma unroll
-        for (int x = 0; x < kX; ++x)
+            for (int x = 0; x < kX; ++x)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const f16x8 vf = codes8<kCodes, f16x8>(vr[x][2 * u], vr[x][2 * u + 1]);
+                for (int u = 0; u < 2; ++u) {
+                    const f16x8 vf = codes8<kCodes, f16x8>(vr[x][2 * u], vr[x][2 * u + 1]);
 #pragma unroll
-                for (int n = 0; n < kNt; ++n) acc[n][x] = mfma(vf, pf[n][u], acc[n][x]);
-            }
-        load_v(after);
-        load_pages(later);
+                    for (int n = 0; n < kNt; ++n) acc[n][x] = mfma(vf, pf[n][u], acc[n][x]);
+                }
+            load_v(after);
+            load_pages(later);
+            t += kWaves;
+        } while (t < t1);
     }
 
     // Join the waves: common references first, then the sums through LDS, each
