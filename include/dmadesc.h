@@ -714,7 +714,8 @@ int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_to
  *   lse        f32[total][heads] or NULL
  *   q_start, total   as dmadesc_kv_append (total * heads < 2^31)
  * Workspace: dmadesc_kv_attend_workspace_bytes(...), for the partial results
- * of requests whose cache is split over several workgroups.
+ * of requests whose cache is split over several workgroups (0 bytes where the
+ * table is too narrow for that; ws may then be NULL).
  */
 #define DMADESC_KV_CAUSAL 1u
 int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride,

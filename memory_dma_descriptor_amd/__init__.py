@@ -771,14 +771,15 @@ def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table:
                    lse=_kv_new((total, heads), torch.float32, dev, stream))
     if ws is None:
         rows, width = table.shape
-        ws = _kv_new(_kv_attend_bytes(total, rows, heads, kv_heads, dim, width, page_tokens),
-                     torch.uint8, dev, stream)
+        need = _kv_attend_bytes(total, rows, heads, kv_heads, dim, width, page_tokens)
+        ws = _kv_new(need, torch.uint8, dev, stream) if need else None
+    ws_bytes = 0 if ws is None else ws.numel()
     rc = lib().dmadesc_kv_attend(
         ctypes.byref(cache), *qp, qs, total, heads, _KV_TYPE[q.dtype],
         KV_CAUSAL if causal else 0, 0.0 if scale is None else scale,
         _dev(out["out"], q.dtype, "out", total * heads * dim),
-        _dev(out["lse"], torch.float32, "lse", total * heads), _dev(ws, torch.uint8, "ws"),
-        ws.numel(), _stream(dev, stream))
+        _dev(out["lse"], torch.float32, "lse", total * heads),
+        _dev(ws, torch.uint8, "ws") if ws_bytes else None, ws_bytes, _stream(dev, stream))
     _check("dmadesc_kv_attend", rc)
     return out
 

@@ -559,7 +559,7 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
             stat[2][wv][n * 16 + col] = l[n];
         }
     }
-    if (blockIdx.x == it.base && threadIdx.x == 0) a.plan[b] = make_uint2(it.base, it.splits);
+    if (a.plan && blockIdx.x == it.base && threadIdx.x == 0) a.plan[b] = make_uint2(it.base, it.splits);
     __syncthreads();
     const bool whole = it.splits == 1;
 #pragma unroll
@@ -945,7 +945,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
         __builtin_amdgcn_s_setprio(0);
     }
 
-    if (blockIdx.x == it.base && tid == 0) a.plan[b] = make_uint2(it.base, it.splits);
+    if (a.plan && blockIdx.x == it.base && tid == 0) a.plan[b] = make_uint2(it.base, it.splits);
     l += __shfl_xor(l, 32, kWave);
     if (!on) return;
     const uint64_t orow = (uint64_t)(s0 + jq) * a.heads + hq;
@@ -1095,7 +1095,7 @@ Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_head
     p.few_part = take(4 * f * p.tile_rows * dim);
     p.many_lse = take(4 * n * kRowsMany);
     p.many_part = take(4 * n * kRowsMany * dim);
-    p.bytes = at;
+    p.bytes = p.join ? at : 0;                       // nothing to join: no partial results, no plan
     return p;
 }
 
@@ -1156,7 +1156,7 @@ hipError_t launch_kv_attend(const KvAttendArgs &k, hipStream_t s)
     few.out = k.out;
     few.lse = k.lse;
     uint8_t *const ws = static_cast<uint8_t *>(k.ws);
-    few.plan = reinterpret_cast<uint2 *>(ws + p.plan_at);
+    few.plan = p.join ? reinterpret_cast<uint2 *>(ws + p.plan_at) : nullptr;
     AttendArgs many = few;
     few.part = reinterpret_cast<float *>(ws + p.few_part);
     few.part_lse = reinterpret_cast<float *>(ws + p.few_lse);

@@ -133,29 +133,41 @@ __global__ __launch_bounds__(kThreads) void k_kv_fork(Table t, const int32_t *pa
 
 // ---------------------------------------------------------------- reserve ---
 
+// Two launches. The first counts the free pages of every chunk of 2,048 and
+// works out what every slot takes, with running sums within chunks of 256
+// slots. In the second, a page's thread knows its rank among the free pages
+// and finds the slot whose ranks hold it (the chunk of slots in LDS, then the
+// slot among 256 running sums), so that no list of free pages is written and
+// read between: a third launch cost 4 us and its call 3 us more. Slots' threads write what does not depend on a page.
 struct ReserveArgs {
     Table t;
     const int32_t *slot, *n_new;
     uint32_t n;
     int32_t *src, *dst;
     uint8_t *status;
+    uint32_t page_chunks, slot_chunks;
     uint32_t *free_count;      // [page chunks] free pages
+    uint8_t *free_bits;        // [page chunks][256] which of a thread's 8 pages are free, on entry
     uint64_t *slot_sum;        // [slot chunks] pages taken
-    uint64_t *nfree;           // free pages of all
-    uint32_t *take;            // [n] pages taken; bit 31: the last page is copied
-    uint32_t *list;            // [npages] free pages by rank
+    uint32_t *take;            // [n] pages taken; bit 31: the last page is copied; kNone: refused
+    uint32_t *upto;            // [n] pages taken by the chunk's slots up to this one
+    uint32_t *from;            // [n] first table column the slot writes
 };
 
 constexpr uint32_t kShared = 1u << 31;
 
+__device__ __forceinline__ uint32_t taken(uint32_t take) { return take == kNone ? 0u : take & ~kShared; }
+
 // What slot i needs: its pages, whether its last page is shared and partly
 // filled; kNone where the slot is refused.
-__device__ __forceinline__ uint32_t slot_take(const ReserveArgs &a, uint32_t i)
+__device__ __forceinline__ uint32_t slot_take(const ReserveArgs &a, uint32_t i, uint32_t &from)
 {
     const Table &t = a.t;
     const int32_t r = a.slot[i];
+    const int64_t add = a.n_new[i];
+    from = 0;
     if (r < 0 || (uint32_t)r >= t.rows) return kNone;
-    const int64_t len = t.lens[r], add = a.n_new[i];
+    const int64_t len = t.lens[r];
     if (add < 0 || !len_ok(t, len) || !len_ok(t, len + add)) return kNone;
     if (add == 0) return 0;
     const uint32_t have = columns(t, len), want = columns(t, len + add);
@@ -165,7 +177,8 @@ __device__ __forceinline__ uint32_t slot_take(const ReserveArgs &a, uint32_t i)
         if (!page_ok(t, last)) return kNone;
         shared = t.refs[last] > 1;
     }
-    return (want - have + (shared ? 1u : 0u)) | (shared ? kShared : 0u);
+    from = have - (shared ? 1u : 0u);
+    return (want - from) | (shared ? kShared : 0u);
 }
 
 // Flags of the chunk's pages in page order: thread k holds pages 8k .. 8k+7.
@@ -193,90 +206,125 @@ __device__ __forceinline__ T block_sum(T v, T *scratch)
     return s;
 }
 
-__global__ __launch_bounds__(kThreads) void k_reserve_count(ReserveArgs a, uint32_t page_chunks)
+__global__ __launch_bounds__(kThreads) void k_reserve_count(ReserveArgs a)
 {
-    __shared__ uint64_t scratch[kThreads / kWave];
-    if (blockIdx.x < page_chunks) {
+    __shared__ uint32_t scratch[kThreads / kWave];
+    if (blockIdx.x < a.page_chunks) {
         const uint32_t f = page_flags(a.t, blockIdx.x, [](uint32_t, int32_t r) { return r == 0; });
-        const uint64_t s = block_sum<uint64_t>(__popc(f), scratch);
-        if (threadIdx.x == 0) a.free_count[blockIdx.x] = (uint32_t)s;
+        const uint32_t s = block_sum<uint32_t>(__popc(f), scratch);
+        a.free_bits[blockIdx.x * kThreads + threadIdx.x] = (uint8_t)f;
+        if (threadIdx.x == 0) a.free_count[blockIdx.x] = s;
         return;
     }
-    const uint32_t chunk = blockIdx.x - page_chunks, i = chunk * kThreads + threadIdx.x;
-    uint32_t take = 0;
+    const uint32_t chunk = blockIdx.x - a.page_chunks, i = chunk * kThreads + threadIdx.x;
+    uint32_t take = 0, from = 0;
+    if (i < a.n) take = slot_take(a, i, from);
+    uint32_t all;
+    const uint32_t before = block_excl_scan<kThreads, uint32_t>(taken(take), scratch, &all);
     if (i < a.n) {
-        take = slot_take(a, i);
         a.take[i] = take;
+        a.from[i] = from;
+        a.upto[i] = before + taken(take);
     }
-    const uint64_t s = block_sum<uint64_t>(take == kNone ? 0u : take & ~kShared, scratch);
-    if (threadIdx.x == 0) a.slot_sum[chunk] = s;
+    if (threadIdx.x == 0) a.slot_sum[chunk] = all;
 }
 
-__global__ __launch_bounds__(kThreads) void k_reserve_list(ReserveArgs a, uint32_t slot_chunks)
-{
-    __shared__ uint64_t scratch[kThreads / kWave];
-    uint64_t before = 0, need = 0;
-    for (uint32_t k = threadIdx.x; k < blockIdx.x; k += kThreads) before += a.free_count[k];
-    for (uint32_t k = threadIdx.x; k < slot_chunks; k += kThreads) need += a.slot_sum[k];
-    before = block_sum(before, scratch);
-    need = block_sum(need, scratch);
-    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0)
-        *a.nfree = before + a.free_count[blockIdx.x];
-    if (before >= need) return;
-    const uint32_t f = page_flags(a.t, blockIdx.x, [](uint32_t, int32_t r) { return r == 0; });
-    __syncthreads();                                   // scratch is read before it is reused
-    uint64_t total;
-    uint64_t rank = before + block_excl_scan<kThreads, uint64_t>(__popc(f), scratch, &total);
-    const uint32_t p0 = blockIdx.x * kChunk + threadIdx.x * kPer;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-        if (f >> k & 1) {
-            if (rank < need) a.list[rank] = p0 + k;
-            ++rank;
-        }
-}
+constexpr uint32_t kSums = 1024;                    // running sums kept in LDS
 
-// One wave per slot.
 __global__ __launch_bounds__(kThreads) void k_reserve_give(ReserveArgs a)
 {
+    __shared__ uint64_t scratch[kThreads / kWave];
+    __shared__ uint64_t sums[kSums];
+    __shared__ uint16_t order[kChunk];
     const Table &t = a.t;
-    const uint32_t i = blockIdx.x * (kThreads / kWave) + wave();
-    if (i >= a.n) return;
-    const uint32_t chunk = i / kThreads;
-    uint64_t before = 0;
-    for (uint32_t k = lane(); k < chunk; k += kWave) before += a.slot_sum[k];
-    for (uint32_t k = chunk * kThreads + lane(); k < i; k += kWave) {
-        const uint32_t v = a.take[k];
-        before += v == kNone ? 0u : v & ~kShared;
+    const bool is_page = blockIdx.x < a.page_chunks;
+    const uint32_t chunk = is_page ? blockIdx.x : blockIdx.x - a.page_chunks;
+
+    uint64_t nfree = 0, before = 0;                 // free pages of all, of the chunks before
+    for (uint32_t k = threadIdx.x; k < a.page_chunks; k += kThreads) {
+        const uint32_t v = a.free_count[k];
+        nfree += v;
+        if (is_page && k < chunk) before += v;
     }
-    before = wave_sum(before);
-    const uint32_t v = a.take[i];
-    const bool shared = v != kNone && (v & kShared) != 0;
-    const uint32_t take = v == kNone ? 0u : v & ~kShared;
-    const bool full = take > 0 && before + take > *a.nfree;
-    if (v == kNone || full) {
-        if (lane() == 0) {
-            a.status[i] = full ? DMADESC_KV_ENOSPC : DMADESC_KV_EINVAL;
-            a.src[i] = a.dst[i] = -1;
-        }
+    nfree = block_sum(nfree, scratch);
+    if (!is_page) {
+        uint64_t first = 0;                         // pages of the slots of the chunks before
+        for (uint32_t k = threadIdx.x; k < chunk; k += kThreads) first += a.slot_sum[k];
+        first = block_sum(first, scratch);
+        const uint32_t i = chunk * kThreads + threadIdx.x;
+        if (i >= a.n) return;
+        const uint32_t v = a.take[i];
+        const bool full = taken(v) > 0 && first + a.upto[i] > nfree;
+        if (v == kNone || full || !(v & kShared)) a.src[i] = a.dst[i] = -1;
+        a.status[i] = v == kNone ? DMADESC_KV_EINVAL : full ? DMADESC_KV_ENOSPC : DMADESC_KV_OK;
+        if (v != kNone && !full) t.lens[a.slot[i]] += a.n_new[i];
         return;
     }
-    const uint32_t r = (uint32_t)a.slot[i];
-    const int64_t len = t.lens[r], add = a.n_new[i];
-    const uint32_t from = columns(t, len) - (shared ? 1u : 0u);
-    int32_t *const tab = t.table + (uint64_t)r * t.width;
-    const int32_t last = shared ? tab[from] : -1;
-    for (uint32_t k = lane(); k < take; k += kWave) {
-        const uint32_t p = a.list[before + k];
-        tab[from + k] = (int32_t)p;
-        t.refs[p] = 1;
-    }
-    if (lane() == 0) {
-        a.src[i] = last;
-        a.dst[i] = shared ? (int32_t)a.list[before] : -1;
-        if (shared) atomicSub(&t.refs[last], 1);
-        t.lens[r] = (int32_t)(len + add);
-        a.status[i] = DMADESC_KV_OK;
+    before = block_sum(before, scratch);
+    // As the first launch found them: references drop in this one.
+    const uint32_t f = a.free_bits[chunk * kThreads + threadIdx.x];
+    __syncthreads();                                // scratch is read before it is reused
+    uint64_t count;
+    const uint64_t rank = before + block_excl_scan<kThreads, uint64_t>(__popc(f), scratch, &count);
+    const uint64_t end = before + count;
+    // The chunk's free pages in rank order, so that every thread takes one rank
+    // at a time: the pages handed out are the first ones, all in a few chunks.
+    for (int k = 0, at = (int)(rank - before); k < kPer; ++k)
+        if (f >> k & 1) order[at++] = (uint16_t)(threadIdx.x * kPer + k);
+
+    // Chunks of slots, kSums at a time; sums[k] is what the slots of chunks up to k take.
+    uint64_t run = 0;
+    for (uint32_t c0 = 0; c0 < a.slot_chunks && run < end; c0 += kSums) {
+        const uint32_t m = a.slot_chunks - c0 < kSums ? a.slot_chunks - c0 : kSums;
+        __syncthreads();
+        const uint64_t start = run;
+        for (uint32_t k0 = 0; k0 < m; k0 += kThreads) {
+            const uint32_t k = k0 + threadIdx.x;
+            const uint64_t v = k < m ? a.slot_sum[c0 + k] : 0;
+            uint64_t all;
+            const uint64_t ex = block_excl_scan<kThreads, uint64_t>(v, scratch, &all);
+            if (k < m) sums[k] = run + ex + v;
+            run += all;
+        }
+        __syncthreads();
+        const uint64_t lo_rank = start > before ? start : before, hi_rank = run < end ? run : end;
+        for (uint64_t mine = lo_rank + threadIdx.x; mine < hi_rank; mine += kThreads) {
+            uint32_t lo = 0, hi = m;                // first chunk of slots with sums > mine
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi) / 2;
+                if (sums[mid] > mine) hi = mid;
+                else lo = mid + 1;
+            }
+            const uint64_t first = lo ? sums[lo - 1] : start;
+            const uint32_t in = (uint32_t)(mine - first);
+            // First slot of it with upto > in: of 16 groups of 16, then of 16 slots, so
+            // that there are two waits and not eight.
+            const uint32_t s0 = (c0 + lo) * kThreads, last_slot = a.n - 1;
+            uint32_t x = s0;
+#pragma unroll
+            for (int step = 16; step >= 1; step /= 16) {
+                uint32_t below = 0;
+#pragma unroll
+                for (uint32_t g = 0; g < 15; ++g) {
+                    const uint32_t at = x + (g + 1) * step - 1;
+                    below += a.upto[at < last_slot ? at : last_slot] <= in ? 1u : 0u;
+                }
+                x += below * step;
+            }
+            const uint32_t v = a.take[x], upto = a.upto[x];
+            if (first + upto > nfree) continue;     // the slot is refused: out of pages
+            const uint32_t at = in - (upto - taken(v));
+            const uint32_t page = chunk * kChunk + order[mine - before];
+            int32_t *const entry = t.table + (uint64_t)(uint32_t)a.slot[x] * t.width + a.from[x] + at;
+            if (at == 0 && (v & kShared)) {
+                const int32_t last = *entry;
+                a.src[x] = last;
+                a.dst[x] = (int32_t)page;
+                atomicSub(&t.refs[last], 1);
+            }
+            *entry = (int32_t)page;
+            t.refs[page] = 1;
+        }
     }
 }
 
@@ -444,8 +492,9 @@ hipError_t launch_kv_fork(const KvPageArgs &k, const int32_t *parent, const int3
 
 size_t ws_kv_reserve(uint64_t npages, uint64_t n)
 {
-    return align256(4ull * chunks_of(npages, kChunk)) + align256(8ull * chunks_of(n, kThreads) + 8) +
-           align256(4ull * n) + align256(4ull * npages);
+    const uint32_t pc = chunks_of(npages, kChunk);
+    return align256(4ull * pc) + align256((size_t)kThreads * pc) +
+           align256(8ull * chunks_of(n, kThreads)) + 3 * align256(4ull * n);
 }
 
 hipError_t launch_kv_reserve(const KvPageArgs &k, const int32_t *slot, const int32_t *n_new,
@@ -453,19 +502,17 @@ hipError_t launch_kv_reserve(const KvPageArgs &k, const int32_t *slot, const int
 {
     const uint32_t pc = chunks_of(k.npages, kChunk), sc = chunks_of(k.n, kThreads);
     uint8_t *p = static_cast<uint8_t *>(ws);
-    ReserveArgs a{table_of(k), slot, n_new, k.n, src, dst, k.status,
-                  nullptr, nullptr, nullptr, nullptr, nullptr};
-    a.free_count = reinterpret_cast<uint32_t *>(p);
-    p += align256(4ull * pc);
-    a.nfree = reinterpret_cast<uint64_t *>(p);
-    a.slot_sum = a.nfree + 1;
-    p += align256(8ull * sc + 8);
-    a.take = reinterpret_cast<uint32_t *>(p);
-    p += align256(4ull * k.n);
-    a.list = reinterpret_cast<uint32_t *>(p);
-    k_reserve_count<<<pc + sc, kThreads, 0, s>>>(a, pc);
-    k_reserve_list<<<pc, kThreads, 0, s>>>(a, sc);
-    k_reserve_give<<<chunks_of(k.n, kThreads / kWave), kThreads, 0, s>>>(a);
+    auto take = [&](size_t bytes) { uint8_t *const r = p; p += align256(bytes); return r; };
+    ReserveArgs a{table_of(k), slot, n_new, k.n, src, dst, k.status, pc, sc,
+                  nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+    a.free_count = reinterpret_cast<uint32_t *>(take(4ull * pc));
+    a.free_bits = take((size_t)kThreads * pc);
+    a.slot_sum = reinterpret_cast<uint64_t *>(take(8ull * sc));
+    a.take = reinterpret_cast<uint32_t *>(take(4ull * k.n));
+    a.upto = reinterpret_cast<uint32_t *>(take(4ull * k.n));
+    a.from = reinterpret_cast<uint32_t *>(take(4ull * k.n));
+    k_reserve_count<<<pc + sc, kThreads, 0, s>>>(a);
+    k_reserve_give<<<pc + sc, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -375,6 +375,33 @@ def test_page_steps(rows, tokens, npages, longest):
     assert (src[n:] == -1).all() and (dst[n:] == -1).all()
 
 
+def test_reserve_many_slots():
+    # More slots than running sums fit LDS (1,024 chunks of 256), pages for all
+    # but the last, each taking a page or replacing a shared one.
+    rows, tokens = 300000, 16
+    rng = np.random.default_rng(8)
+    table = np.full((rows, 2), -1, np.int32)
+    lens = rng.choice([0, 0, 16, 3], rows).astype(np.int32)
+    held = np.nonzero(lens)[0]
+    npages = len(held) + 100000
+    refs = np.zeros(npages, np.int32)
+    pages = rng.permutation(npages)[:len(held)].astype(np.int32)
+    pages[1::2] = pages[:len(pages) // 2 * 2:2]              # pairs of rows share a page
+    table[held, 0] = pages
+    np.add.at(refs, pages, 1)
+    state = (refs, table, lens)
+    gpu = on_gpu(*state)
+    slots = rng.permutation(rows).astype(np.int32)
+    news = rng.integers(0, 20, rows).astype(np.int32)
+    src, dst, status = kc.reserve(*state, slots, news, tokens)
+    assert (status == 3).any() and (status == 0).any() and (src >= 0).any()
+    r = dd.kv_reserve(*gpu, i32(slots), i32(news), tokens, check=False)
+    assert np.array_equal(r["status"].cpu().numpy(), status)
+    assert np.array_equal(r["src"].cpu().numpy(), src)
+    assert np.array_equal(r["dst"].cpu().numpy(), dst)
+    same_state(gpu, state)
+
+
 def test_reserve_runs_out_and_refuses():
     refs, table, lens = on_gpu(np.array([1, 0, 0, 0, 1], np.int32),
                                np.array([[0, -1, -1, -1], [4, -1, -1, -1], [-1] * 4], np.int32),

@@ -68,9 +68,11 @@ def test_append_arguments():
 @no_gpu_only
 def test_attend_arguments():
     lib = dd.lib()
-    need = lib.dmadesc_kv_attend_workspace_bytes(4, 2, 4, 2, 64, 4, 32)
+    size = lib.dmadesc_kv_attend_workspace_bytes
+    need = size(4, 2, 4, 2, 64, 128, 32)
     assert need > 0 and need % 256 == 0
-    ok = [cache(), P, 256, 64, P, 4, 4, 0, 1, 0.0, P, P, P, need, NULL]
+    assert size(4, 2, 4, 2, 64, 4, 32) == 0                   # 128 tokens are never split
+    ok = [cache(width=128), P, 256, 64, P, 4, 4, 0, 1, 0.0, P, P, P, need, NULL]
     for k, bad in [(0, NULL), (1, NULL), (1, P + 8), (2, 4), (2, -8), (3, 12), (4, NULL),
                    (5, 1 << 31), (6, 0), (6, 3), (7, 2), (8, 2), (9, float("nan")), (10, NULL),
                    (10, P + 8), (11, P + 1), (12, NULL), (12, P + 16), (13, need - 1)]:
@@ -126,8 +128,8 @@ def test_workspaces_grow_with_their_sizes():
     assert 0 < ws(dd.OP_KV_RESERVE, 0, 1) < ws(dd.OP_KV_RESERVE, 10000, 1) \
         < ws(dd.OP_KV_RESERVE, 10000, 5000)
     assert 0 < ws(dd.OP_KV_COMPACT, 0) < ws(dd.OP_KV_COMPACT, 10000)
-    # every free page's id, every page's mover number
-    assert ws(dd.OP_KV_RESERVE, 10000, 1) > 40000 and ws(dd.OP_KV_COMPACT, 10000) > 40000
+    # a bit of every page, three words of every slot; every page's mover number
+    assert ws(dd.OP_KV_RESERVE, 10000, 5000) > 1250 + 60000 and ws(dd.OP_KV_COMPACT, 10000) > 40000
 
 
 def test_binding_refuses_wrong_tensors():
