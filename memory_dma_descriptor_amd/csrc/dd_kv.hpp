@@ -82,5 +82,35 @@ __device__ __forceinline__ uint32_t kv_request_of(uint32_t rows, uint64_t i, Fir
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// The request of item i, where request b's items start at number
+// q_start[b] / 16 + 2 b, with its span and length. As kv_request_of, but the
+// last probe loads the span's end and the length beside its start, so that
+// they cost no further round.
+__device__ __forceinline__ uint32_t kv_blocks_of(const KvView &c, const int32_t *q_start,
+                                                 uint32_t total, uint64_t i, uint32_t &s0,
+                                                 uint32_t &s1, int &len)
+{
+    uint32_t lo = 0, n = c.rows;
+    for (;;) {
+        const uint32_t step = (n + kWave - 1) / kWave;
+        const uint64_t at = (uint64_t)lane() * step;
+        const uint32_t r = lo + (at < n ? (uint32_t)at : 0u);
+        uint32_t a, z;
+        kv_span(q_start, r, total, a, z);
+        const int l = step == 1 ? kv_len(c, r) : 0;
+        const bool in = at < n && (uint64_t)(a / kBlock) + 2ull * r <= i;
+        const int k = __popcll(__ballot(in));
+        const uint32_t skip = (uint32_t)(k > 0 ? k - 1 : 0);
+        if (step == 1) {
+            s0 = (uint32_t)__builtin_amdgcn_readlane((int)a, (int)skip);
+            s1 = (uint32_t)__builtin_amdgcn_readlane((int)z, (int)skip);
+            len = __builtin_amdgcn_readlane(l, (int)skip);
+            return __builtin_amdgcn_readfirstlane(lo + skip);
+        }
+        lo += skip * step;
+        n = n - skip * step < step ? n - skip * step : step;
+    }
+}
+
 }  // namespace
 }  // namespace dd

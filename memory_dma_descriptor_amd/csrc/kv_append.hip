@@ -20,6 +20,8 @@
 // stores in the page's own order and nothing passes through LDS.
 // Bound: HBM bytes for prompts, the chain of dependent loads (q_start, lens,
 // table, block) for single tokens.
+#include <type_traits>
+
 #include "dd_internal.h"
 #include "dd_kv.hpp"
 
@@ -35,37 +37,24 @@ struct AppendArgs {
     uint32_t items;                         // block numbers
 };
 
-// kN consecutive values as f32.
+// kN consecutive values as they lie in memory, and as f32.
 template <int kType, int kN>
-__device__ __forceinline__ void load_values(const void *p, int64_t at, float (&x)[kN])
-{
-    if constexpr (kType == DMADESC_KV_FP32) {
-        const float *q = static_cast<const float *>(p) + at;
-        if constexpr (kN >= 4) {
-#pragma unroll
-            for (int i = 0; i < kN; i += 4) {
-                const f32x4 t = *reinterpret_cast<const f32x4 *>(q + i);
-                x[i] = t[0]; x[i + 1] = t[1]; x[i + 2] = t[2]; x[i + 3] = t[3];
-            }
-        } else if constexpr (kN == 2) {
-            const f32x2 t = *reinterpret_cast<const f32x2 *>(q);
-            x[0] = t[0]; x[1] = t[1];
-        } else {
-            x[0] = q[0];
-        }
-    } else {
-        const uint16_t *q = static_cast<const uint16_t *>(p) + at;
-        uint16_t h[kN];
-        __builtin_memcpy(h, __builtin_assume_aligned(q, 2 * kN), 2 * kN);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            if constexpr (kType == DMADESC_KV_BF16)
-                x[i] = __uint_as_float((uint32_t)h[i] << 16);
-            else
-                x[i] = (float)__builtin_bit_cast(_Float16, h[i]);
-        }
+struct Raw {
+    typedef typename std::conditional<kType == DMADESC_KV_FP32, float, uint16_t>::type T;
+    T v[kN];
+
+    __device__ __forceinline__ void load(const void *p, int64_t at)
+    {
+        __builtin_memcpy(v, __builtin_assume_aligned(static_cast<const T *>(p) + at,
+                                                     sizeof(v) < 16 ? sizeof(v) : 16), sizeof(v));
     }
-}
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (kType == DMADESC_KV_FP32) return v[i];
+        else if constexpr (kType == DMADESC_KV_BF16) return __uint_as_float((uint32_t)v[i] << 16);
+        else return (float)__builtin_bit_cast(_Float16, v[i]);
+    }
+};
 
 // |x|, or 0 where x takes no part in the maximum (infinite or NaN).
 __device__ __forceinline__ float finite_abs(float x)
@@ -143,54 +132,58 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
     const uint32_t is_v = (uint32_t)(unit / c.kv_heads) & 1u;
     const uint32_t item = (uint32_t)(unit / c.kv_heads / 2);
     if (item >= a.items) return;
-    const uint32_t b = kv_request_of(c.rows, item, [&](uint32_t r) {
-        const int32_t s = a.q_start[r];
-        const uint32_t u = s < 0 ? 0u : ((uint32_t)s > a.total ? a.total : (uint32_t)s);
-        return (uint64_t)(u / kBlock) + 2ull * r;
-    });
     uint32_t s0, s1;
-    kv_span(a.q_start, b, a.total, s0, s1);
+    int len;
+    const uint32_t b = kv_blocks_of(c, a.q_start, a.total, item, s0, s1, len);
     const int64_t nth = (int64_t)item - ((int64_t)(s0 / kBlock) + 2 * (int64_t)b);
-    const int len = kv_len(c, b), count = (int)(s1 - s0), first = len - count;
-    if (nth < 0 || count <= 0 || first < 0) return;
+    const int count = (int)(s1 - s0), first = len - count;
+    if (nth < 0 || count <= 0 || first < 0 || nth > (len - 1) / kBlock) return;
     const int block = first / kBlock + (int)nth;
-    if (nth > (len - 1) / kBlock || block > (len - 1) / kBlock) return;
+    if (block > (len - 1) / kBlock) return;
     const int per = (int)c.tshift - 4;
-    const int32_t page = c.table[(uint64_t)b * c.width + ((uint32_t)block >> per)];
-    if (page < 0 || (uint32_t)page >= c.npages) return;
     const uint32_t sub = (uint32_t)block & ((1u << per) - 1u);
-
-    uint8_t *const base = c.pool + (uint64_t)page * c.page_bytes;
-    float *const scale = reinterpret_cast<float *>(base + 2ull * c.code_bytes) +
-                         (is_v ? c.scales : 0u) + ((head << per) + sub);
-    uint8_t *const codes = base + (is_v ? c.code_bytes : 0u) +
-                           (uint64_t)((head << per) + sub) * (kBlock * kD);
     const int old = first - block * kBlock;            // tokens 0..old-1 were there before
     const int end = len - block * kBlock;              // tokens end..15 are zero
     const int64_t tok0 = (int64_t)s0 + (int64_t)block * kBlock - first;   // token of place 0
-    int e_old = kMinExp;
-    if (old > 0) e_old = (int)((__float_as_uint(*scale) >> 23) & 0xffu) - 127;
     const int ln = lane();
+
+    // The page is asked for here and waited for after the values are under way.
+    const int32_t page = c.table[(uint64_t)b * c.width + ((uint32_t)block >> per)];
+    auto block_of = [&](float *&scale) -> uint8_t * {
+        uint8_t *const base = c.pool + (uint64_t)(uint32_t)page * c.page_bytes;
+        scale = reinterpret_cast<float *>(base + 2ull * c.code_bytes) + (is_v ? c.scales : 0u) +
+                ((head << per) + sub);
+        return base + (is_v ? c.code_bytes : 0u) + (uint64_t)((head << per) + sub) * (kBlock * kD);
+    };
+    float *scale;
+    int e_old = kMinExp;
+    // Every place loads a new token, its own or the nearest, so that all loads
+    // are in flight at once; a conditional load would be waited for where it stands.
+    auto clamp = [&](int r) { return r < old ? (old < 0 ? 0 : old) : r < end ? r : end - 1; };
 
     if (!is_v) {
         constexpr int kLanes = kD / 8;                 // lanes of a row
         constexpr int kRows = kWave / kLanes;          // rows a round
         constexpr int kRounds = kBlock / kRows;
         const int r0 = ln / kLanes, d0 = (ln % kLanes) * 8;
+        Raw<kType, 8> raw[kRounds];
         float x[kRounds][8];
         float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i)
+            raw[i].load(a.k, (tok0 + clamp(i * kRows + r0)) * a.k_tok + head * a.k_head + d0);
+        if (page < 0 || (uint32_t)page >= c.npages) return;
+        uint8_t *const codes = block_of(scale);
+        if (old > 0) e_old = (int)((__float_as_uint(*scale) >> 23) & 0xffu) - 127;
 #pragma unroll
         for (int i = 0; i < kRounds; ++i) {
             const int r = i * kRows + r0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
-            if (r >= old && r < end)
-                load_values<kType, 8>(a.k, (tok0 + r) * a.k_tok + head * a.k_head + d0, x[i]);
+            for (int j = 0; j < 8; ++j) {
+                x[i][j] = r >= old && r < end ? raw[i].get(j) : 0.0f;
+                m = fmaxf(m, finite_abs(x[i][j]));
+            }
         }
-#pragma unroll
-        for (int i = 0; i < kRounds; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(x[i][j]));
         const int e_new = block_exp<kCodes>(wave_max(m));
         const int e = e_new > e_old ? e_new : e_old;
         const float up = pow2(-e), again = pow2(e_old - e);
@@ -215,28 +208,37 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
         if (ln == 0) *scale = pow2(e);
     } else {
         constexpr int kDims = kD / kWave;              // dimensions of a lane
+        Raw<kType, kDims> raw[kBlock];
         float x[kBlock][kDims];
         float m = 0.0f;
 #pragma unroll
-        for (int r = 0; r < kBlock; ++r) {
+        for (int r = 0; r < kBlock; ++r)
+            raw[r].load(a.v, (tok0 + clamp(r)) * a.v_tok + head * a.v_head + ln * kDims);
+        if (page < 0 || (uint32_t)page >= c.npages) return;
+        uint8_t *const codes = block_of(scale);
+        u32x4 *const at = reinterpret_cast<u32x4 *>(codes + ln * kDims * kBlock);
+        u32x4 held[kDims];                             // earlier tokens' codes
+        if (old > 0) {
 #pragma unroll
-            for (int j = 0; j < kDims; ++j) x[r][j] = 0.0f;
-            if (r >= old && r < end)
-                load_values<kType, kDims>(a.v, (tok0 + r) * a.v_tok + head * a.v_head + ln * kDims,
-                                          x[r]);
+            for (int j = 0; j < kDims; ++j) held[j] = at[j];
+            e_old = (int)((__float_as_uint(*scale) >> 23) & 0xffu) - 127;
+        } else {
+#pragma unroll
+            for (int j = 0; j < kDims; ++j) held[j] = u32x4{0, 0, 0, 0};
         }
 #pragma unroll
         for (int r = 0; r < kBlock; ++r)
 #pragma unroll
-            for (int j = 0; j < kDims; ++j) m = fmaxf(m, finite_abs(x[r][j]));
+            for (int j = 0; j < kDims; ++j) {
+                x[r][j] = r >= old && r < end ? raw[r].get(j) : 0.0f;
+                m = fmaxf(m, finite_abs(x[r][j]));
+            }
         const int e_new = block_exp<kCodes>(wave_max(m));
         const int e = e_new > e_old ? e_new : e_old;
         const float up = pow2(-e), again = pow2(e_old - e);
-        u32x4 *const at = reinterpret_cast<u32x4 *>(codes + ln * kDims * kBlock);
 #pragma unroll
         for (int j = 0; j < kDims; ++j) {
-            u32x4 w = {0, 0, 0, 0};
-            if (old > 0) w = at[j];
+            const u32x4 w = held[j];
             u32x4 o;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
