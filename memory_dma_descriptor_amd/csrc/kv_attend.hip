@@ -36,8 +36,12 @@ constexpr int few_occupancy(int dim, int nt)   // waves a SIMD, by the registers
 {
     return dim * nt <= 64 ? 3 : dim * nt <= 128 ? 2 : 1;
 }
-constexpr uint32_t slots_few(int dim, int nt) { return 512u * few_occupancy(dim, nt); }
+// Products' row tiles that a workgroup of few rows may take: 48 rows, 32 where the
+// accumulators and the join's LDS allow no more.
+constexpr int most_tiles(int dim) { return dim <= 128 ? 3 : 2; }
+constexpr uint32_t slots_few(int dim, int nt) { return 256u * few_occupancy(dim, nt); }
 constexpr uint32_t slots_many(int dim) { return dim == 64 ? 768 : dim == 128 ? 512 : 256; }
+constexpr uint32_t kLongFew = 32, kLongMany = ~0u;      // tiles of a piece past which two rounds run
 constexpr uint32_t kWholeFew = 32, kWholeMany = 8;      // tiles up to which nothing is split
 constexpr uint32_t kMaxSplits = 256;
 constexpr uint32_t kRowsMany = 128;         // query rows of a workgroup of the kernel of many
@@ -122,14 +126,22 @@ __device__ __forceinline__ V8 codes8(uint32_t lo, uint32_t hi)
     return V8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Most pieces of `base` unsplit ones when `aim` are aimed at.
+__host__ __device__ constexpr uint32_t most_pieces(uint32_t base, uint32_t aim)
+{
+    return base < aim ? aim : base + aim / 2;
+}
+
 // What a call's requests are cut into: about as many pieces as workgroups fit
-// the card at once (kSlots), so that they run in one round of equal pieces, but
+// the card at once (kSlots), so that they run in one round of equal pieces, or
+// in two where they are longer than kLong tiles (kLong = 32 for few rows: 64
+// requests of 200 to 9,000 tokens take 134 us in two rounds, 148 in one), but
 // no piece below kLeast tiles, and nothing where no request has more than kWhole:
 // the join costs 5 us, what a wave needs for about eight tiles. The
 // host knows only bounds, so every workgroup adds the lengths up for itself and
 // finds its own piece, which costs less than a launch that would do it once:
 // up to 64 requests are one load and a few lane exchanges of each wave.
-template <int kRows, int kThreads, uint32_t kSlots, uint32_t kLeast, uint32_t kWhole>
+template <int kRows, int kThreads, uint32_t kSlots, uint32_t kLeast, uint32_t kWhole, uint32_t kLong>
 struct Plan {
     static constexpr int kWaves = kThreads / kWave;
 
@@ -158,22 +170,31 @@ struct Plan {
         return s < 1 ? 1u : (s > kMaxSplits ? kMaxSplits : s);
     }
 
-    // Tiles of a piece for `work` tiles in `base` unsplit pieces: a request's last
-    // piece is half full on the average.
-    static __device__ __forceinline__ uint32_t first_chunk(float work, float base, bool whole)
+    // Tiles of a piece for `work` tiles in `base` unsplit pieces (a request's last
+    // piece is half full on the average), and how many pieces are aimed at.
+    static __device__ __forceinline__ uint32_t first_chunk(float work, float base, bool whole, uint32_t &aim)
     {
+        aim = kSlots;
         if (whole) return kWhole;
-        const float room = fmaxf((float)kSlots - 0.5f * base, 0.25f * kSlots);
-        const float c = ceilf(work / room);
+        float c = ceilf(work / fmaxf((float)kSlots - 0.5f * base, 0.25f * kSlots));
+        if (c > (float)kLong) {
+            aim = 2 * kSlots;
+            c = ceilf(work / fmaxf(2.0f * kSlots - 0.5f * base, 0.5f * kSlots));
+        }
         return c < (float)kLeast ? kLeast : (uint32_t)c;
     }
 
-    static __device__ __forceinline__ bool fits(uint32_t pieces, float base)
+    // Pieces are made longer until they are no more than this (the host sizes the
+    // grid by it); if a few rounds do not do, nothing is split.
+    static __device__ __forceinline__ bool fits(uint32_t pieces, float base, uint32_t aim)
     {
-        return pieces <= kSlots || base >= (float)kSlots;
+        return pieces <= most_pieces((uint32_t)base, aim);
     }
-
-    static __device__ __forceinline__ uint32_t larger(uint32_t chunk) { return chunk + chunk / 16 + 1; }
+    static __device__ __forceinline__ uint32_t larger(uint32_t chunk, int round)
+    {
+        return round < kRounds ? chunk + chunk / 16 + 1 : 1u << 30;
+    }
+    static constexpr int kRounds = 12;
 
     static __device__ __forceinline__ Item item(const Size &z, uint32_t b, uint32_t at, uint32_t k,
                                                 uint32_t parts, uint32_t heads)
@@ -191,10 +212,11 @@ struct Plan {
             const Size z = size(a, (uint32_t)lane());
             const float work = wave_sum((float)z.rts * (float)z.tiles) * (float)heads;
             const float base = wave_sum((float)z.rts) * (float)heads;
-            uint32_t chunk = first_chunk(work, base, __ballot(z.rts > 0 && z.tiles > kWhole) == 0);
+            uint32_t aim;
+            uint32_t chunk = first_chunk(work, base, __ballot(z.rts > 0 && z.tiles > kWhole) == 0, aim);
             uint32_t mine = z.rts * splits(z, chunk) * heads, upto = wave_incl_scan(mine);
-            for (int k = 0; k < 4 && !fits(__builtin_amdgcn_readlane(upto, kWave - 1), base); ++k) {
-                chunk = larger(chunk);
+            for (int k = 0; k <= kRounds && !fits(__builtin_amdgcn_readlane(upto, kWave - 1), base, aim); ++k) {
+                chunk = larger(chunk, k);
                 mine = z.rts * splits(z, chunk) * heads;
                 upto = wave_incl_scan(mine);
             }
@@ -236,8 +258,9 @@ struct Plan {
         }
         work *= (float)heads;
         base *= (float)heads;
-        uint32_t chunk = first_chunk(work, base, large == 0);
-        for (int k = 0; k < 4; ++k) {
+        uint32_t aim;
+        uint32_t chunk = first_chunk(work, base, large == 0, aim);
+        for (int k = 0; k <= kRounds; ++k) {
             uint32_t n = 0;
             for (uint32_t b = threadIdx.x; b < rows; b += kThreads) {
                 const Size z = size(a, b);
@@ -250,8 +273,8 @@ struct Plan {
             n = 0;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) n += scan[w];
-            if (fits(n, base)) break;
-            chunk = larger(chunk);
+            if (fits(n, base, aim)) break;
+            chunk = larger(chunk, k);
         }
         uint64_t run = 0;
         for (uint32_t b0 = 0; b0 < rows; b0 += kThreads) {
@@ -332,12 +355,12 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
     constexpr int kC = kD / 64;             // 64-dimension pieces of a key row
     constexpr int kX = kD / 16;             // 16-dimension pieces of the output
     typedef typename QFrag<kQ>::type Q8;
-    __shared__ f32x4 obuf[kWaves][kX][kWave];
+    __shared__ f32x4 obuf[kWaves][kNt * kX][kWave];
     __shared__ float stat[3][kWaves][kRows];
     __shared__ int first_nan[kD];
 
     Item it;
-    if (!Plan<kRows, kThreads, slots_few(kD, kNt), 8, kWholeFew>::find(a, blockIdx.x, it)) return;
+    if (!Plan<kRows, kThreads, slots_few(kD, kNt), 8, kWholeFew, kLongFew>::find(a, blockIdx.x, it)) return;
     for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
     __syncthreads();
     const KvView &c = a.c;
@@ -352,10 +375,10 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
     const int per = (int)c.tshift - 4;
     const uint32_t sub_mask = (1u << per) - 1u;
 
-    // The lane's query rows (operand columns) and the last token each sees.
+    // The lane's query rows (operand columns) and the last token each sees; a
+    // column past the last row computes row 0 with nothing seen.
     Q8 qf[kNt][kC][2];
     int limit[kNt];
-    uint64_t orow[kNt];
     int low = len - 1, high = len - 1;      // least and largest limit of the tile's rows
     if (a.causal) {
         const uint32_t last = nrows - 1 < row0 + kRows - 1 ? nrows - 1 : row0 + kRows - 1;
@@ -368,17 +391,13 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
         const bool on = r < nrows;
         const uint32_t rr = on ? r : 0u, j = rr / a.group, h = head * a.group + rr % a.group;
         limit[n] = !on ? -1 : a.causal ? len - news + (int)j : len - 1;
-        orow[n] = ((uint64_t)(s0 + j) * a.heads + h) * kD;
         const uint16_t *const q = static_cast<const uint16_t *>(a.q) +
                                   (int64_t)(s0 + j) * a.q_tok + (int64_t)h * a.q_head + 16 * g;
 #pragma unroll
         for (int k = 0; k < kC; ++k)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                u32x4 w = {0, 0, 0, 0};
-                if (on) w = *reinterpret_cast<const u32x4 *>(q + 64 * k + 8 * u);
-                qf[n][k][u] = __builtin_bit_cast(Q8, w);
-            }
+            for (int u = 0; u < 2; ++u)
+                qf[n][k][u] = __builtin_bit_cast(Q8, *reinterpret_cast<const u32x4 *>(q + 64 * k + 8 * u));
     }
 
     f32x4 acc[kNt][kX];
@@ -561,9 +580,21 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
     }
     if (a.plan && blockIdx.x == it.base && threadIdx.x == 0) a.plan[b] = make_uint2(it.base, it.splits);
     __syncthreads();
-    const bool whole = it.splits == 1;
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
+        float mxa = -kInf;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) mxa = fmaxf(mxa, stat[1][w][n * 16 + col]);
+        const float mine = exp2_(mx[n] - (mxa == -kInf ? 0.0f : mxa));
+#pragma unroll
+        for (int x = 0; x < kX; ++x) obuf[wv][n * kX + x][ln] = acc[n][x] * mine;
+    }
+    __syncthreads();
+    const bool whole = it.splits == 1;
+#pragma unroll 1
+    for (int n = 0; n < kNt; ++n) {
+        const uint32_t r = row0 + n * 16 + col;
+        if (r >= nrows) break;                      // the lane's rows ascend
         float ma = -kInf, mxa = -kInf, la = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
@@ -574,33 +605,30 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
 #pragma unroll
         for (int w = 0; w < kWaves; ++w)
             la += stat[2][w][n * 16 + col] * exp2_(stat[0][w][n * 16 + col] - ms);
-        const float mine = exp2_(mx[n] - mxs);
-        if (n > 0) __syncthreads();                 // the sums of n - 1 are read
-#pragma unroll
-        for (int x = 0; x < kX; ++x) obuf[wv][x][ln] = acc[n][x] * mine;
-        __syncthreads();
         // A row that sees nothing: zero, and no mass (la = 0).
         const float norm = la == 0.0f ? 0.0f : exp2_(mxs - ms - kShift) / la;
         const float lse2 = la == 0.0f ? -kInf : ms + __builtin_log2f(la);
         const uint64_t prow = (uint64_t)blockIdx.x * kRows + n * 16 + col;   // of the partial results
-        if (row0 + n * 16 + col < nrows) {
-            for (int x = wv; x < kX; x += kWaves) {
-                f32x4 o = obuf[0][x][ln];
+        const uint32_t j = r / a.group;
+        const uint64_t orow = (uint64_t)(s0 + j) * a.heads + head * a.group + r % a.group;
+        const int lim = a.causal ? len - news + (int)j : len - 1;
+#pragma unroll 1
+        for (int x = wv; x < kX; x += kWaves) {
+            f32x4 o = obuf[0][n * kX + x][ln];
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) o += obuf[w][x][ln];
-                o *= norm;
-                if (kCodes == DMADESC_KV_E4M3) {
+            for (int w = 1; w < kWaves; ++w) o += obuf[w][n * kX + x][ln];
+            o *= norm;
+            if (kCodes == DMADESC_KV_E4M3) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (first_nan[16 * x + 4 * g + i] <= limit[n]) o[i] = __builtin_nanf("");
-                }
-                if (whole) store4<kQ>(a.out, orow[n] + 16 * x + 4 * g, o);
-                else *reinterpret_cast<f32x4 *>(a.part + prow * kD + 16 * x + 4 * g) = o;
+                for (int i = 0; i < 4; ++i)
+                    if (first_nan[16 * x + 4 * g + i] <= lim) o[i] = __builtin_nanf("");
             }
-            if (wv == 0 && g == 0) {
-                if (!whole) a.part_lse[prow] = lse2;
-                else if (a.lse) a.lse[orow[n] / kD] = lse2 * 0.69314718055994531f;
-            }
+            if (whole) store4<kQ>(a.out, orow * kD + 16 * x + 4 * g, o);
+            else *reinterpret_cast<f32x4 *>(a.part + prow * kD + 16 * x + 4 * g) = o;
+        }
+        if (wv == 0 && g == 0) {
+            if (!whole) a.part_lse[prow] = lse2;
+            else if (a.lse) a.lse[orow] = lse2 * 0.69314718055994531f;
         }
     }
 }
@@ -661,7 +689,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     __shared__ int first_nan[kD];
 
     Item it;
-    if (!Plan<kRows, kThreads, slots_many(kD), 4, kWholeMany>::find(a, blockIdx.x, it)) return;
+    if (!Plan<kRows, kThreads, slots_many(kD), 4, kWholeMany, kLongMany>::find(a, blockIdx.x, it)) return;
     for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
     __syncthreads();
     const KvView &c = a.c;
@@ -700,11 +728,8 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
                                   (int64_t)(s0 + jq) * a.q_tok + (int64_t)hq * a.q_head + 8 * h;
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;   // a negative scale turns q round
 #pragma unroll
-        for (int k = 0; k < kK; ++k) {
-            u32x4 w = {0, 0, 0, 0};
-            if (on) w = *reinterpret_cast<const u32x4 *>(q + 16 * k) ^ flip;
-            qf[k] = __builtin_bit_cast(Q8, w);
-        }
+        for (int k = 0; k < kK; ++k)
+            qf[k] = __builtin_bit_cast(Q8, *reinterpret_cast<const u32x4 *>(q + 16 * k) ^ flip);
     }
     const float scale = fabsf(a.scale);
 
@@ -1051,13 +1076,12 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(AttendArgs few, AttendArgs
 }
 
 // How a call's memory and launches follow from what the host knows, which is
-// not the requests' own sizes. Where a request has more than 32 query rows per
-// key head on the average, the kernel of many rows takes them all (its reads of
+// not the requests' own sizes. Where a request has more than 48 (32 for D = 256)
+// query rows per key head on the average, the kernel of many rows takes them all (its reads of
 // the cache are as good as the other's); otherwise the kernel of few rows does.
-// Only where some request may have more than 256 rows beside those few, a chunk
+// Only where some request may have more than 1,024 rows beside those few, a chunk
 // of a prompt among single tokens, are both launched and share the requests: an
-// idle launch costs 5 us, and a request of up to 256 rows as much as that in the
-// wrong kernel.
+// idle launch costs 4 us.
 struct Launch {
     uint32_t tile_rows;          // of the kernel of few rows: one product's 16, or 32
     uint32_t few, many;          // workgroups (= partial results) of each kernel
@@ -1074,18 +1098,24 @@ Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_head
     const uint64_t mean = (total + rows - 1) / rows * group;
     const uint64_t tiles = (tokens + kTile - 1) / kTile;
     const bool split_few = tiles > kWholeFew, split_many = tiles > kWholeMany;
-    const bool few = mean <= 48, both = few && total > rows && (total - rows) * group > 256;
+    const bool few = mean <= 16u * most_tiles((int)dim), both = few && total > rows && (total - rows) * group > 1024;
     p.most = !few ? 0u : both ? kMostFew : ~0u;
     p.tile_rows = mean <= 16 ? 16u : mean <= 32 ? 32u : 48u;
-    // The even pieces, and one more for each row tile of each key head: at most
-    // all rows' whole tiles and one of each request.
+    // Unsplit pieces: a row tile of a key head each; all rows' whole tiles and one
+    // more of each request at most.
     const uint64_t few_rows = both && all > rows * (uint64_t)kMostFew ? rows * (uint64_t)kMostFew : all;
     const uint64_t big = both ? all / (kMostFew + 1) : rows;      // requests that have many
+    auto grid = [&](uint64_t base, bool split, uint32_t slots, uint32_t long_) -> uint32_t {
+        if (!split) return (uint32_t)base;
+        const uint32_t one = most_pieces((uint32_t)base, slots), two = most_pieces((uint32_t)base, 2 * slots);
+        return base * tiles > (uint64_t)long_ * slots / 4 && two > one ? two : one;
+    };
     if (few)
-        p.few = (uint32_t)((split_few ? slots_few((int)dim, (int)p.tile_rows / 16) : 0u) + kv_heads * (few_rows / p.tile_rows + rows));
+        p.few = grid(kv_heads * (few_rows / p.tile_rows + rows), split_few,
+                     slots_few((int)dim, (int)p.tile_rows / 16), kLongFew);
     if (!few || both)
-        p.many = (uint32_t)((split_many ? slots_many((int)dim) : 0u) +
-                            kv_heads * (all / kRowsMany + (big < rows ? big : rows)));
+        p.many = grid(kv_heads * (all / kRowsMany + (big < rows ? big : rows)), split_many,
+                      slots_many((int)dim), kLongMany);
     if ((p.few && split_few) || (p.many && split_many))
         p.join = (uint32_t)(kv_heads * (all / kJoinRows + rows));
     size_t at = align256(8ull * rows);
@@ -1106,7 +1136,7 @@ void launch_all(const AttendArgs &few, const AttendArgs &many, const Launch &p, 
     if (p.few) {
         if (p.tile_rows == 16) k_kv_attend<kD, kQ, kCodes, 1><<<p.few, kThreads, 0, s>>>(few);
         else if (p.tile_rows == 32) k_kv_attend<kD, kQ, kCodes, 2><<<p.few, kThreads, 0, s>>>(few);
-        else k_kv_attend<kD, kQ, kCodes, 3><<<p.few, kThreads, 0, s>>>(few);
+        else k_kv_attend<kD, kQ, kCodes, most_tiles(kD)><<<p.few, kThreads, 0, s>>>(few);
     }
     if (p.join)
         k_kv_join<kD, kQ><<<p.join, kThreads, 0, s>>>(few, many, p.tile_rows);
