@@ -1010,12 +1010,14 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
 // some of the splits. The chunks of 16 are numbered without a scan: request b's
 // first is q_start[b] * group / 16 + b.
 constexpr uint32_t kJoinRows = 16;
+// Threads of its workgroups: few rows have many splits each, many rows few.
+constexpr uint32_t kJoinFew = 512, kJoinMany = 256;
 
-template <int kD, int kQ>
-__global__ __launch_bounds__(kThreads) void k_kv_join(AttendArgs few, AttendArgs many,
+template <int kD, int kQ, int kJoinThreads>
+__global__ __launch_bounds__(kJoinThreads) void k_kv_join(AttendArgs few, AttendArgs many,
                                                      uint32_t tile_rows)
 {
-    constexpr uint32_t kLanes = kD / 4, kGroups = kThreads / kLanes;
+    constexpr uint32_t kLanes = kD / 4, kGroups = kJoinThreads / kLanes;
     __shared__ f32x4 osum[kGroups][kLanes];
     __shared__ float wsum[kGroups];
     const uint32_t head = blockIdx.x % few.c.kv_heads, chunk = blockIdx.x / few.c.kv_heads;
@@ -1145,8 +1147,10 @@ void launch_all(const AttendArgs &few, const AttendArgs &many, const Launch &p, 
         else if (p.tile_rows == 32) k_kv_attend<kD, kQ, kCodes, 2><<<p.few, kThreads, 0, s>>>(few);
         else k_kv_attend<kD, kQ, kCodes, most_tiles(kD)><<<p.few, kThreads, 0, s>>>(few);
     }
-    if (p.join)
-        k_kv_join<kD, kQ><<<p.join, kThreads, 0, s>>>(few, many, p.tile_rows);
+    if (p.join && p.few)
+        k_kv_join<kD, kQ, kJoinFew><<<p.join, kJoinFew, 0, s>>>(few, many, p.tile_rows);
+    else if (p.join)
+        k_kv_join<kD, kQ, kJoinMany><<<p.join, kJoinMany, 0, s>>>(few, many, p.tile_rows);
 }
 
 template <int kD>
