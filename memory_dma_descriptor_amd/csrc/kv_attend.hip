@@ -129,7 +129,7 @@ __device__ __forceinline__ V8 codes8(uint32_t lo, uint32_t hi)
 // Most pieces of `base` unsplit ones when `aim` are aimed at.
 __host__ __device__ constexpr uint32_t most_pieces(uint32_t base, uint32_t aim)
 {
-    return base < aim ? aim : base + aim / 2;
+    return base < aim ? aim + aim / 8 : base + aim / 2;
 }
 
 // What a call's requests are cut into: about as many pieces as workgroups fit
@@ -184,17 +184,19 @@ struct Plan {
         return c < (float)kLeast ? kLeast : (uint32_t)c;
     }
 
-    // Pieces are made longer until they are no more than this (the host sizes the
-    // grid by it); if a few rounds do not do, nothing is split.
-    static __device__ __forceinline__ bool fits(uint32_t pieces, float base, uint32_t aim)
+    // Round `round` of looking for a piece length: a little longer each time until
+    // the pieces are no more than aimed at. Where that does not come out (requests
+    // of one length double their pieces at once), an eighth more will do, and where
+    // that does not either, nothing is split. The host sizes the grid by most_pieces.
+    static constexpr int kStrict = 4, kRounds = 12;
+    static __device__ __forceinline__ bool fits(uint32_t pieces, float base, uint32_t aim, int round)
     {
-        return pieces <= most_pieces((uint32_t)base, aim);
+        return pieces <= (round <= kStrict && base < (float)aim ? aim : most_pieces((uint32_t)base, aim));
     }
-    static __device__ __forceinline__ uint32_t larger(uint32_t chunk, int round)
+    static __device__ __forceinline__ uint32_t larger(uint32_t chunk, uint32_t first, int round)
     {
-        return round < kRounds ? chunk + chunk / 16 + 1 : 1u << 30;
+        return round == kStrict ? first : round < kRounds ? chunk + chunk / 16 + 1 : 1u << 30;
     }
-    static constexpr int kRounds = 12;
 
     static __device__ __forceinline__ Item item(const Size &z, uint32_t b, uint32_t at, uint32_t k,
                                                 uint32_t parts, uint32_t heads)
@@ -214,9 +216,10 @@ struct Plan {
             const float base = wave_sum((float)z.rts) * (float)heads;
             uint32_t aim;
             uint32_t chunk = first_chunk(work, base, __ballot(z.rts > 0 && z.tiles > kWhole) == 0, aim);
+            const uint32_t first = chunk;
             uint32_t mine = z.rts * splits(z, chunk) * heads, upto = wave_incl_scan(mine);
-            for (int k = 0; k <= kRounds && !fits(__builtin_amdgcn_readlane(upto, kWave - 1), base, aim); ++k) {
-                chunk = larger(chunk, k);
+            for (int k = 0; k <= kRounds && !fits(__builtin_amdgcn_readlane(upto, kWave - 1), base, aim, k); ++k) {
+                chunk = larger(chunk, first, k);
                 mine = z.rts * splits(z, chunk) * heads;
                 upto = wave_incl_scan(mine);
             }
@@ -260,6 +263,7 @@ struct Plan {
         base *= (float)heads;
         uint32_t aim;
         uint32_t chunk = first_chunk(work, base, large == 0, aim);
+        const uint32_t first = chunk;
         for (int k = 0; k <= kRounds; ++k) {
             uint32_t n = 0;
             for (uint32_t b = threadIdx.x; b < rows; b += kThreads) {
@@ -273,8 +277,8 @@ struct Plan {
             n = 0;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) n += scan[w];
-            if (fits(n, base, aim)) break;
-            chunk = larger(chunk, k);
+            if (fits(n, base, aim, k)) break;
+            chunk = larger(chunk, first, k);
         }
         uint64_t run = 0;
         for (uint32_t b0 = 0; b0 < rows; b0 += kThreads) {
