@@ -84,8 +84,9 @@
  *               its static scratch allows.
  *    Errors in individual requests are not call errors: they are reported
  *    per request in an output column (stated per call).
- *  - All arithmetic is exact unsigned 64-bit integer arithmetic; outputs are
- *    bit-for-bit deterministic (no atomics decide any output position).
+ *  - All arithmetic is exact unsigned 64-bit integer arithmetic (the cache's
+ *    calls: as stated there); outputs are bit-for-bit deterministic (no atomics
+ *    decide any output position).
  *  - `ws` is a caller-owned device workspace of at least
  *    dmadesc_workspace_bytes(op, n, param) bytes, 256-byte aligned (-EINVAL
  *    otherwise). Its contents on entry are ignored and on return are

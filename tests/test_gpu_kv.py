@@ -223,6 +223,15 @@ def test_attend_many_requests():
     check_attend(list(lens), list(news), 1, 2, 16, 64, kc.INT8, "fp16")
 
 
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+def test_attend_a_chunk_among_single_tokens(codes):
+    # Few rows on the average and one request of many: both kernels and the join
+    # share the requests. Requests of 32 and 33 tokens lie on either side.
+    lens = [5 + 7 * i for i in range(60)] + [900, 3000, 64, 65, 400]
+    news = [1] * 60 + [600, 1, 32, 33, 0]
+    check_attend(lens, news, 1, 2, 32, 64, codes, "bf16")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
 def test_attend_scales_far_apart(dtype, codes):
