@@ -1025,8 +1025,10 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
 // some of the splits. The chunks of 16 are numbered without a scan: request b's
 // first is q_start[b] * group / 16 + b.
 constexpr uint32_t kJoinRows = 16;
-// Threads of its workgroups: few rows have many splits each, many rows few.
-constexpr uint32_t kJoinFew = 512, kJoinMany = 256;
+// Threads of its workgroups: 512 where they all run at once (420 of them: 5.0 us,
+// with 256 threads 6.2), 256 where they are many and most find nothing to join
+// (4,000: 5.3 us, with 512 threads 9.6).
+constexpr uint32_t kJoinWide = 512, kJoinNarrow = 256, kJoinOnce = 1024;
 
 template <int kD, int kQ, int kJoinThreads>
 __global__ __launch_bounds__(kJoinThreads) void k_kv_join(AttendArgs few, AttendArgs many,
@@ -1161,10 +1163,10 @@ void launch_all(const AttendArgs &few, const AttendArgs &many, const Launch &p, 
         if (p.tile_rows == 16) k_kv_attend<kD, kQ, kCodes, 1><<<p.few, kThreads, 0, s>>>(few);
         else k_kv_attend<kD, kQ, kCodes, 2><<<p.few, kThreads, 0, s>>>(few);
     }
-    if (p.join && p.few)
-        k_kv_join<kD, kQ, kJoinFew><<<p.join, kJoinFew, 0, s>>>(few, many, p.tile_rows);
+    if (p.join && p.join <= kJoinOnce)
+        k_kv_join<kD, kQ, kJoinWide><<<p.join, kJoinWide, 0, s>>>(few, many, p.tile_rows);
     else if (p.join)
-        k_kv_join<kD, kQ, kJoinMany><<<p.join, kJoinMany, 0, s>>>(few, many, p.tile_rows);
+        k_kv_join<kD, kQ, kJoinNarrow><<<p.join, kJoinNarrow, 0, s>>>(few, many, p.tile_rows);
 }
 
 template <int kD>

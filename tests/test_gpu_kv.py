@@ -286,6 +286,24 @@ def test_attend_refuses_and_spares_bad_pages():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+def test_attend_many_rows_spares_bad_pages(codes):
+    # Prompts whose table names pages outside the pool, beside a good one.
+    tokens, dim = 16, 128
+    rng = np.random.default_rng(4)
+    pool = torch.from_numpy(random_pool(rng, 12, 1, tokens, dim, codes)).cuda()
+    q = torch.randn((150, 2, dim), device="cuda", dtype=torch.bfloat16)
+    lens, start = i32([60, 100, 50]), i32([0, 60, 100, 150])
+    table = i32([[-1, 12, 1 << 30, -(1 << 31)] + [-1] * 4, [0, 1, -5, 3, 99, 5, 6] + [-1],
+                 [7, 8, 9, 10] + [-1] * 4])
+    st = dd.kv_check(start, 150, pool, table, lens, 1, tokens, dim)
+    assert st.tolist() == [dd.KV_EPAGE, dd.KV_EPAGE, dd.KV_OK]
+    r = dd.kv_attend(q, start, pool, table, lens, 1, tokens, codes=codes, check=False)
+    good = dd.kv_attend(q[100:], i32([0, 50]), pool, table[2:].contiguous(), lens[2:].contiguous(), 1,
+                        tokens, codes=codes)
+    assert torch.equal(r["out"][100:], good["out"]) and torch.equal(r["lse"][100:], good["lse"])
+
+
 def test_attend_past_four_gigabytes():
     # Pages on both sides of 2^32 bytes of the pool.
     heads, tokens, dim = 8, 128, 128
