@@ -706,7 +706,9 @@ int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_to
  * being the request's new tokens. A row that sees nothing gets o = 0 and
  * lse = -inf. What lies past the length or is not seen never counts, whatever
  * bits it holds. Scores, softmax and sums are f32; the probabilities are
- * rounded to 11 bits for the product with V.
+ * rounded to 11 bits for the product with V, relative to the row's largest
+ * probability times V scale: terms below 2^-27 of that keep fewer bits, terms
+ * below 2^-37 may count as 0 in o (never in lse).
  *   q          [total][heads][dim] of `type` (bf16 or fp16), strides in
  *              elements; base 16-byte aligned, strides multiples of 8
  *   heads      a multiple of kv_heads

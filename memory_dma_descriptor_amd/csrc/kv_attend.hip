@@ -684,9 +684,11 @@ __device__ __forceinline__ float half_max(float x)
 // Here the vector unit has as much to do as the matrix unit (a tile of a wave:
 // 1,024 cycles of products, about 210 vector instructions, 32 of them
 // exponentials), so that three things are done differently. The softmax takes one
-// reference per row, the running maximum M of s + e: 2^(s + e - M + 6) is both the
+// reference per row, the running maximum M of s + e: 2^(s + e - M + 13) is both the
 // f16 probability and, times 2^-e once per block, the term of the sum; it moves
-// only when a row passes it by 2^8, so that the accumulators are seldom rescaled.
+// only when a row passes it by 2^2, so that the accumulators are seldom rescaled
+// (by 2^8, with terms that much nearer f16's end, took the same time): 11 bits
+// down to 2^-27 of the row's largest term, fewer to 2^-37, nothing below.
 // (Where scales lie beyond 2^-40..2^40 a term could vanish in the one and matter
 // in the other; from the first such tile on the sum is taken from exponentials of
 // its own.) The next codes are converted between the first product's
@@ -703,7 +705,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     constexpr int kChunkStride = kTile * 16 + 16;   // 8 dimensions of 64 tokens, and a bank step
     constexpr int kLoads = kTile * kD / 16 / kThreads;   // 16-byte loads of a thread, K and V each
     constexpr int kPieces = kD;                     // 16-byte pieces of a block
-    constexpr float kRise = 8.0f, kLift = 6.0f;
+    constexpr float kRise = 2.0f, kLift = 13.0f;
     typedef typename QFrag<kQ>::type Q8;
     __shared__ __align__(16) uint8_t kbuf[2][kD / 8 * kChunkStride];
     __shared__ __align__(16) uint8_t vbuf[2][kTile * kD * 2];
