@@ -694,7 +694,7 @@ __device__ __forceinline__ float half_max(float x)
 // its own.) The next codes are converted between the first product's
 // instructions and a block's exponentials taken between the second's. And a wave
 // in a product goes before the other wave of its SIMD. 2,048 tokens over 16,384,
-// 32 heads on 8, D = 128, e4m3: 530 us, 970 TFLOP/s (a library product of 8192^3:
+// 32 heads on 8, D = 128, e4m3: 547 us, 943 TFLOP/s (a library product of 8192^3:
 // 1,217); matrix and vector units are each busy half of the time.
 template <int kD, int kQ, int kCodes>
 __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_kv_attend_many(AttendArgs a)
