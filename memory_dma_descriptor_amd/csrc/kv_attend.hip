@@ -44,7 +44,10 @@ constexpr uint32_t kWholeFew = 20, kWholeMany = 4;      // tiles up to which not
 constexpr uint32_t kMaxSplits = 256;
 constexpr uint32_t kRowsMany = 128;         // query rows of a workgroup of the kernel of many
 constexpr uint32_t kMostFew = 64;           // rows up to which a request is the first's, if both run
-constexpr float kShift = 15.0f;             // probabilities are at most 2^15 in f16
+constexpr float kShift = 15.0f;             // probabilities are at most 2^14 in f16, see ve
+// Log of the largest factor of an exponential: what f32 loses of one below 2^-126
+// is then below f16's least step.
+constexpr float kFar = 100.0f;
 
 struct AttendArgs {
     KvView c;
@@ -506,13 +509,13 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
 #pragma unroll
                         for (int n = 0; n < kNt; ++n) s[n][j] = mfma(kf, qf[n][k][u], s[n][j]);
                     }
-            const float kscale = ks * a.scale, vscale = vs;
+            const float kscale = ks * a.scale;
+            const float ve = (float)((int)(__float_as_uint(vs) >> 23 & 0xffu) - 126);
             const int nvalid = valid;
             load_k(after, more);
 
             const int tok = t * kTile + g * kBlock;       // first token of the lane's block
             const bool edge = t * kTile + kTile - 1 > low;   // some row does not see the whole tile
-            const float ve = (float)((int)(__float_as_uint(vscale) >> 23 & 0xffu) - 126);
             f16x8 pf[kNt][2];
 #pragma unroll
             for (int n = 0; n < kNt; ++n) {
@@ -533,17 +536,21 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
                 topv = fmaxf(topv, __shfl_xor(topv, 32, kWave));
                 const float mn = fmaxf(m[n], top), mxn = fmaxf(mx[n], topv);
                 const float ms = mn == -kInf ? 0.0f : mn, mxs = mxn == -kInf ? 0.0f : mxn;
-                const float f = nvalid == 0 ? 0.0f : vscale * exp2_(ms - mxs + kShift);
+                // The probability in f16 is p 2^rise. Where rise is large (a V scale far
+                // above that of the row's largest score) part of it, h, goes into the
+                // exponential, so that neither factor leaves f32's range.
+                const float rise = ve + (ms - mxs) + (kShift - 1.0f);
+                const float h = fmaxf(rise - kFar, 0.0f), f = exp2_(rise - h), from = ms - h;
                 float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float p = exp2_(s[n][j][i] - ms);
+                        const float p = exp2_(s[n][j][i] - from);
                         sum += p;
                         pf[n][j >> 1][(j & 1) * 4 + i] = (_Float16)(p * f);
                     }
-                l[n] = l[n] * exp2_(m[n] - ms) + sum;
+                l[n] = __builtin_fmaf(sum, exp2_(-h), l[n] * exp2_(m[n] - ms));
                 const float back = exp2_(mx[n] - mxs);
                 m[n] = mn;
                 mx[n] = mxn;

@@ -1,0 +1,135 @@
+"""The cache's attention at the ends of its ranges, on the GPU against the
+definition in 64 bits: block scales and score factors far apart, in the kernel
+of few rows, the kernel of many rows and the join of split requests."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import memory_dma_descriptor_amd as dd
+from tests import kv_cases as kc
+from tests.gpu_cases import say
+from tests.test_gpu_kv import i32, make_table, random_pool, starts
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(pool, table, lens, news, q, kv, tokens, codes, causal, scale):
+    """kc.attend's outputs, and for the bound: `top`, the row's largest probability
+    times V scale, and `codes`, the sum of |V code| over the tokens it sees."""
+    total, heads, dim = q.shape
+    group = heads // kv
+    zero = lambda *s: np.zeros((total, heads) + s)                           # noqa: E731
+    r = dict(out=zero(dim), mass=zero(dim), codes=zero(dim), top=zero(), size=zero(),
+             lse=zero() - math.inf)
+    at = 0
+    for b, (length, n) in enumerate(zip(lens, news)):
+        if length and n:
+            k, v = kc.request_cache(pool, table[b], length, kv, tokens, dim, codes)
+            _, vc, _, vs = kc.split_page(np.ascontiguousarray(pool[table[b, :kc.columns(length, tokens)]]),
+                                         kv, tokens, dim)
+            vc = np.abs(kc.TABLE[codes][vc]).transpose(0, 2, 4, 1, 3).reshape(-1, kv, dim)[:length]
+            vs = np.repeat(vs.astype(np.float64).transpose(0, 2, 1), kc.BLOCK, axis=1)
+            vs = vs.reshape(-1, kv)[:length]
+            limit = (length - n + np.arange(n)) if causal else np.full(n, length - 1)
+            seen = np.arange(length) <= limit[:, None]
+            some = seen.any(1)
+            for h in range(heads):
+                g, rows = h // group, np.arange(at, at + n)[some]
+                see = seen[some]
+                s = np.where(see, q[rows, h] @ k[:, g].T * scale, -math.inf)
+                top = s.max(1)
+                lse = top + np.log(np.exp(s - top[:, None]).sum(1))
+                p = np.exp(s - lse[:, None])
+                r["out"][rows, h], r["mass"][rows, h] = p @ v[:, g], p @ np.abs(v[:, g])
+                r["codes"][rows, h] = see @ vc[:, g]
+                r["top"][rows, h] = (p * vs[:, g]).max(1)
+                size = np.abs(q[rows, h]) @ np.abs(k[:, g]).T * abs(scale)
+                r["size"][rows, h] = np.where(see, size, 0).max(1)
+                r["lse"][rows, h] = lse
+        at += n
+    return r
+
+
+def bounds(ref, dim, longest, dtype, exps):
+    """kc.attend_bounds with what far scales add. A probability is rounded in f16
+    relative to the row's largest probability times V scale, which stands at 2^13
+    or more there: half of f16's least step, 2^-25, is 2^-38 of it for each unit
+    of a code. The exponentials' arguments hold scores and exponents together: at
+    most eight roundings of half a step of (|score| + |exponent|) each, where 16
+    more cover the offsets 13, 15 and 32."""
+    out, lse = kc.attend_bounds(ref, dim, longest, dtype)
+    arg = 8 * 2.0 ** -24 * (ref["size"] + max(abs(e) for e in exps) + 16)
+    err = arg[..., None] * ref["mass"] + 2.0 ** -38 * ref["top"][..., None] * ref["codes"]
+    return out + err * (1 + torch.finfo(dtype).eps / 2), lse + arg
+
+
+def check(pool, table, lens, news, q, kv, tokens, codes, exps, causal=True, scale=None):
+    """q: numpy float32 [total, heads, dim], cast to bf16 (whose range holds the values)."""
+    dim = q.shape[2]
+    q = torch.from_numpy(q).bfloat16()
+    ref = reference(pool, table, lens, news, q.double().numpy(), kv, tokens, codes, causal,
+                    1 / math.sqrt(dim) if scale is None else scale)
+    args = (q.cuda(), i32(starts(news)), torch.from_numpy(pool).cuda(), i32(table), i32(lens), kv, tokens)
+    r = dd.kv_attend(*args, codes=codes, causal=causal, scale=scale)
+    out, lse = r["out"].double().cpu().numpy(), r["lse"].double().cpu().numpy()
+    bound, lse_bound = bounds(ref, dim, max(lens), q.dtype, exps)
+    empty = np.isneginf(ref["lse"])
+    assert np.isfinite(out).all() and np.array_equal(np.isneginf(lse), empty)
+    assert (out[empty] == 0).all()
+    d = np.abs(out - ref["out"]) / bound
+    with np.errstate(invalid="ignore"):
+        dl = np.abs(lse - ref["lse"]) / lse_bound
+    say(f"  worst out {d.max():.3f}, lse {np.nanmax(dl, initial=0):.3f} of the bound")
+    assert d.max() <= 1 and np.nanmax(dl, initial=0) <= 1
+    again = dd.kv_attend(*args, codes=codes, causal=causal, scale=scale)
+    assert torch.equal(again["out"], r["out"]) and torch.equal(again["lse"], r["lse"])
+
+
+def far_cache(rng, lens, kv, tokens, dim, codes, far, gap, first_far, spare=1, extra=1):
+    """A cache whose tokens before first_far have zero values (scale 2^-64, as
+    kv_append writes them) and score 0 under one_hot queries, and whose later ones
+    have values under 2^far and score -gap."""
+    npages = sum(kc.columns(n, tokens) for n in lens) + spare
+    pool = random_pool(rng, npages, kv, tokens, dim, codes)
+    table = make_table(rng, lens, tokens, npages, extra)
+    kcodes, vcodes, ks, vs = kc.split_page(pool, kv, tokens, dim)
+    ks[:], kcodes[:], vs[:] = 1.0, 0, 2.0 ** far
+    for b, n in enumerate(lens):
+        for t in range(n):
+            p = table[b, t // tokens]
+            if t < first_far:
+                vcodes[p, :, t % tokens // 16, :, t % 16] = 0
+                vs[p, :, t % tokens // 16] = 2.0 ** -64
+            else:
+                kcodes[p, :, t % tokens, 0] = kc.nearest([-float(gap)], codes)[0]
+    return pool, table
+
+
+def one_hot(total, heads, dim):
+    q = np.zeros((total, heads, dim), np.float32)
+    q[:, :, 0] = 1
+    return q
+
+
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("far", [-20, 50, 80, 119])
+@pytest.mark.parametrize("gap", [0, 40, 88, 112])
+def test_few_rows_zero_values_beside_large_ones(codes, causal, far, gap):
+    # Rows that see the zero values alone, with the large ones hidden in the same
+    # tile, and rows that see both, in one tile and in several.
+    say(f"few far {codes} {causal} 2^{far} gap {gap}")
+    rng = np.random.default_rng(1000 + far + gap)
+    for dim, lens, news, first in ((64, [36], [8], 32), (128, [400, 52], [3, 6], 48), (256, [67], [5], 64)):
+        pool, table = far_cache(rng, lens, 2, 16, dim, codes, far, gap, first)
+        check(pool, table, lens, news, one_hot(sum(news), 4, dim), 2, 16, codes, (-64, far), causal, 1.0)
+
+
+def test_few_rows_that_see_nothing_beside_large_values():
+    rng = np.random.default_rng(0)
+    pool, table = far_cache(rng, [5, 20], 1, 16, 64, kc.INT8, 119, 0, 0)
+    check(pool, table, [5, 20], [9, 4], one_hot(13, 2, 64), 1, 16, kc.INT8, (-64, 119), True, 1.0)
