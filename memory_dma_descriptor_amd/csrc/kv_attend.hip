@@ -509,13 +509,13 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
 #pragma unroll
                         for (int n = 0; n < kNt; ++n) s[n][j] = mfma(kf, qf[n][k][u], s[n][j]);
                     }
-            const float kscale = ks * a.scale;
-            const float ve = (float)((int)(__float_as_uint(vs) >> 23 & 0xffu) - 126);
+            const float kscale = ks * a.scale, vscale = vs;
             const int nvalid = valid;
             load_k(after, more);
 
             const int tok = t * kTile + g * kBlock;       // first token of the lane's block
             const bool edge = t * kTile + kTile - 1 > low;   // some row does not see the whole tile
+            const float ve = (float)((int)(__float_as_uint(vscale) >> 23 & 0xffu) - 126);
             f16x8 pf[kNt][2];
 #pragma unroll
             for (int n = 0; n < kNt; ++n) {
@@ -536,11 +536,13 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
                 topv = fmaxf(topv, __shfl_xor(topv, 32, kWave));
                 const float mn = fmaxf(m[n], top), mxn = fmaxf(mx[n], topv);
                 const float ms = mn == -kInf ? 0.0f : mn, mxs = mxn == -kInf ? 0.0f : mxn;
-                // The probability in f16 is p 2^rise. Where rise is large (a V scale far
-                // above that of the row's largest score) part of it, h, goes into the
-                // exponential, so that neither factor leaves f32's range.
-                const float rise = ve + (ms - mxs) + (kShift - 1.0f);
-                const float h = fmaxf(rise - kFar, 0.0f), f = exp2_(rise - h), from = ms - h;
+                // The probability in f16 is p f. Where f would be large (a V scale far above
+                // that of the row's largest score) part of it, 2^h, goes into the
+                // exponential, so that neither factor leaves f32's range. f is written with
+                // the scale itself: from its exponent alone the compiler takes the scale
+                // earlier and waits for it before the loads of V (3 % of a long cache's time).
+                const float rise = ms - mxs + kShift, h = fmaxf(rise + ve - kFar, 0.0f);
+                const float f = nvalid == 0 ? 0.0f : vscale * exp2_(rise - h), from = ms - h;
                 float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
