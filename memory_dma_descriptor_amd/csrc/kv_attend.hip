@@ -1047,7 +1047,6 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv_join(AttendArgs few, Attend
 {
     constexpr uint32_t kLanes = kD / 4, kGroups = kJoinThreads / kLanes;
     __shared__ f32x4 osum[kGroups][kLanes];
-    __shared__ float wsum[kGroups];
     const uint32_t head = blockIdx.x % few.c.kv_heads, chunk = blockIdx.x / few.c.kv_heads;
     const uint32_t b = kv_request_of(few.c.rows, chunk, [&](uint32_t r) {
         const int32_t s = few.q_start[r];
@@ -1078,35 +1077,43 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv_join(AttendArgs few, Attend
         const uint32_t row = base + grp % width;
         const bool on = phase < share && row < rows;
         const uint64_t in = (uint32_t)r0 % tile_rows + row;
-        float top = -kInf, w = 0.0f;
+        float top = -kInf, all = 0.0f;
         f32x4 o = {0, 0, 0, 0};
         if (on) {
-            for (uint32_t s = at; s < plan.y; s += kLanes)
-                top = fmaxf(top, a.part_lse[(uint64_t)(first + s * step) * tile_rows + in]);
+            float mine = -kInf;
+            for (uint32_t s = at; s < plan.y; s += kLanes) {
+                const float x = a.part_lse[(uint64_t)(first + s * step) * tile_rows + in];
+                top = fmaxf(mine, x);
+                const float ref = top == -kInf ? 0.0f : top;
+                all = all * exp2_(mine - ref) + exp2_(x - ref);
+                mine = top;
+            }
 #pragma unroll
             for (int d = (int)kLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kLanes));
             if (top == -kInf) top = 0.0f;
+            all *= exp2_(mine - top);
+#pragma unroll
+            for (int d = (int)kLanes / 2; d > 0; d >>= 1) all += __shfl_xor(all, d, kLanes);
+            // Parts count by their share of the row's mass. Shares sum to 1, so that no
+            // sum leaves the range of its parts; they are taken in two factors, since one
+            // alone may lie below f32's range where its part's values are large.
+            const float inv = all == 0.0f ? 0.0f : 1.0f / all;
 #pragma unroll 4
             for (uint32_t s = phase; s < plan.y; s += share) {
                 const uint64_t p = (uint64_t)(first + s * step) * tile_rows + in;
-                const float v = exp2_(a.part_lse[p] - top);
-                w += v;
-                o += *reinterpret_cast<const f32x4 *>(a.part + p * kD + at * 4) * v;
+                const float v = exp2_(0.5f * (a.part_lse[p] - top));
+                o += *reinterpret_cast<const f32x4 *>(a.part + p * kD + at * 4) * v * (v * inv);
             }
         }
         osum[grp][at] = o;
-        if (at == 0) wsum[grp] = w;
         __syncthreads();
         if (on && phase == 0) {
-            for (uint32_t k = 1; k < share; ++k) {
-                o += osum[grp + k * width][at];
-                w += wsum[grp + k * width];
-            }
+            for (uint32_t k = 1; k < share; ++k) o += osum[grp + k * width][at];
             const uint32_t r = (uint32_t)r0 + row;
             const uint64_t orow = (uint64_t)(s0 + r / a.group) * a.heads + head * a.group + r % a.group;
-            store4<kQ>(a.out, orow * kD + at * 4, o * (w == 0.0f ? 0.0f : 1.0f / w));
+            store4<kQ>(a.out, orow * kD + at * 4, o);
             if (a.lse && at == 0)
-                a.lse[orow] = w == 0.0f ? -kInf : (top + __builtin_log2f(w)) * 0.69314718055994531f;
+                a.lse[orow] = all == 0.0f ? -kInf : (top + __builtin_log2f(all)) * 0.69314718055994531f;
         }
         __syncthreads();
     }

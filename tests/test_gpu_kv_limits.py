@@ -133,3 +133,24 @@ def test_few_rows_that_see_nothing_beside_large_values():
     rng = np.random.default_rng(0)
     pool, table = far_cache(rng, [5, 20], 1, 16, 64, kc.INT8, 119, 0, 0)
     check(pool, table, [5, 20], [9, 4], one_hot(13, 2, 64), 1, 16, kc.INT8, (-64, 119), True, 1.0)
+
+
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+@pytest.mark.parametrize("far,gap", [(50, 0), (50, 88), (61, 0), (80, 0), (119, 0), (119, 40), (119, 112)])
+def test_join_of_far_scales(codes, far, gap):
+    # The zero values in one piece of a split request, the large ones in another,
+    # whose weight alone is below f32's range.
+    say(f"join far {codes} 2^{far} gap {gap}")
+    rng = np.random.default_rng(1000 + far + gap)
+    for lens, first in (([6000, 30], 3008), ([6000, 30], 5920)):
+        pool, table = far_cache(rng, lens, 1, 64, 64, codes, far, gap, first)
+        check(pool, table, lens, [1, 1], one_hot(2, 2, 64), 1, 64, codes, (-64, far), True, 1.0)
+
+
+def test_join_of_the_largest_values():
+    # Partial outputs that are all near f32's largest number.
+    rng = np.random.default_rng(1)
+    pool, table = far_cache(rng, [6000], 1, 64, 64, kc.INT8, 120, 0, 0)
+    _, vcodes, _, _ = kc.split_page(pool, 1, 64, 64)
+    vcodes[:] = 127
+    check(pool, table, [6000], [1], one_hot(1, 2, 64), 1, 64, kc.INT8, (120, 120), True, 1.0)
