@@ -715,10 +715,14 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     constexpr int kLoads = kTile * kD / 16 / kThreads;   // 16-byte loads of a thread, K and V each
     constexpr int kPieces = kD;                     // 16-byte pieces of a block
     constexpr float kRise = 2.0f, kLift = 13.0f;
+    // The sum l stands 2^kSum above its terms relative to M. They may lie as far from M
+    // as V scales lie from 1: with scales of 2^-64 to 2^127 and 2^29 tokens l stays
+    // inside f32's range, and so does what matters of it 2^-30 further down.
+    constexpr float kSum = 32.0f;
     typedef typename QFrag<kQ>::type Q8;
     __shared__ __align__(16) uint8_t kbuf[2][kD / 8 * kChunkStride];
     __shared__ __align__(16) uint8_t vbuf[2][kTile * kD * 2];
-    __shared__ float scales[2][3][4];   // [buffer][scale of K, exponent of V, 2^-that][block]
+    __shared__ float scales[2][3][4];   // [buffer][scale of K, exponent of V, 2^(kSum - kLift - that)][block]
     __shared__ int first_nan[kD];
 
     Item it;
@@ -854,7 +858,8 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
                 scales[buf][0][tid] = fmaxf(s * scale, 1.17549435e-38f);
             } else {
                 scales[buf][1][tid - 4] = (float)e;
-                scales[buf][2][tid - 4] = __uint_as_float((uint32_t)(e < 127 ? 127 - e : 1) << 23);
+                const int back = 127 + (int)(kSum - kLift) - e;
+                scales[buf][2][tid - 4] = __uint_as_float((uint32_t)(back < 254 ? back : 254) << 23);
             }
         }
     };
@@ -956,8 +961,10 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
         tv = half_max(tv);
         if (__ballot(tv > mx + kRise)) {
             const float mxn = fmaxf(mx, tv);
-            const float by = mxn == -kInf ? 1.0f : exp2_(mx - mxn);
-            l *= by;
+            // In two factors: where M rises over the whole range of scales, one alone
+            // would lie below f32's range and l, which need not be small then, be lost.
+            const float half = mxn == -kInf ? 1.0f : exp2_(0.5f * (mx - mxn)), by = half * half;
+            l = l * half * half;
             mx = mxn;
 #pragma unroll
             for (int x = 0; x < kX; ++x) acc[x] *= by;
@@ -968,7 +975,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
             for (int i = 0; i < 4; ++i) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    l += exp2_(__builtin_fmaf(s[i >> 1][(i & 1) * 8 + k], ks[i], -ref));
+                    l += exp2_(__builtin_fmaf(s[i >> 1][(i & 1) * 8 + k], ks[i], kSum - kLift - ref));
                 back[i] = 0.0f;
             }
         }
@@ -1008,8 +1015,8 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     if (!on) return;
     const uint64_t orow = (uint64_t)(s0 + jq) * a.heads + hq;
     const uint64_t prow = (uint64_t)blockIdx.x * kRows + (r - row0);
-    const float norm = l == 0.0f ? 0.0f : 1.0f / l;
-    const float lse2 = l == 0.0f ? -kInf : mx - kLift + __builtin_log2f(l);
+    const float norm = l == 0.0f ? 0.0f : exp2_(kSum - kLift) / l;
+    const float lse2 = l == 0.0f ? -kInf : mx - kSum + __builtin_log2f(l);
 #pragma unroll
     for (int x = 0; x < kX; ++x)
 #pragma unroll

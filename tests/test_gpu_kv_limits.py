@@ -154,3 +154,29 @@ def test_join_of_the_largest_values():
     _, vcodes, _, _ = kc.split_page(pool, 1, 64, 64)
     vcodes[:] = 127
     check(pool, table, [6000], [1], one_hot(1, 2, 64), 1, 64, kc.INT8, (120, 120), True, 1.0)
+
+
+# Requests of this size, two heads on one, run in the kernel of many rows: the
+# first pair with its cache cut into pieces, the second whole.
+MANY = [([700, 500], [90, 120], 2), ([200, 150], [90, 120], 1)]
+
+
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("far,gap", [(-20, 40), (50, 0), (50, 88), (61, 0), (63, 0), (80, 0), (119, 0),
+                                     (119, 40), (119, 112)])
+def test_many_rows_zero_values_beside_large_ones(codes, causal, far, gap):
+    say(f"many far {codes} {causal} 2^{far} gap {gap}")
+    rng = np.random.default_rng(1000 + far + gap)
+    for (lens, news, extra), dim in zip(MANY, (64, 128)):
+        pool, table = far_cache(rng, lens, 1, 64, dim, codes, far, gap, 128, extra=extra)
+        check(pool, table, lens, news, one_hot(sum(news), 2, dim), 1, 64, codes, (-64, far), causal, 1.0)
+
+
+def test_many_rows_of_the_largest_values():
+    rng = np.random.default_rng(1)
+    for lens, news, extra in MANY:
+        pool, table = far_cache(rng, lens, 1, 64, 64, kc.INT8, 120, 0, 0, extra=extra)
+        _, vcodes, _, _ = kc.split_page(pool, 1, 64, 64)
+        vcodes[:] = 127
+        check(pool, table, lens, news, one_hot(sum(news), 2, 64), 1, 64, kc.INT8, (120, 120), True, 1.0)
