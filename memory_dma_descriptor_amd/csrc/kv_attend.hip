@@ -57,6 +57,7 @@ struct AttendArgs {
     uint32_t total, heads, group;
     int causal;
     float scale;                            // times log2 e
+    float most_scale;                       // of K under which the product with scale is finite
     void *out;
     float *lse;
     float *part;                            // [slots][rows of a tile][dim] partial outputs
@@ -509,9 +510,11 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
 #pragma unroll
                         for (int n = 0; n < kNt; ++n) s[n][j] = mfma(kf, qf[n][k][u], s[n][j]);
                     }
-            const float kscale = ks * a.scale, vscale = vs;
             const int nvalid = valid;
             load_k(after, more);
+            // Finite, so that a score of 0 stays one. (Taken before the loads of K, the
+            // compiler waits for the scale between them.)
+            const float kscale = fminf(ks, a.most_scale) * a.scale, vscale = vs;
 
             const int tok = t * kTile + g * kBlock;       // first token of the lane's block
             const bool edge = t * kTile + kTile - 1 > low;   // some row does not see the whole tile
@@ -854,8 +857,8 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
             const float s = (t * 4 + (tid & 3)) * kBlock < len ? sc : 1.0f;
             const int e = (int)(__float_as_uint(s) >> 23 & 0xffu) - 127;
             if (tid < 4) {
-                // Never 0, so that a masked -inf stays one.
-                scales[buf][0][tid] = fmaxf(s * scale, 1.17549435e-38f);
+                // Never 0, so that a masked -inf stays one, and finite, so that a 0 does.
+                scales[buf][0][tid] = fmaxf(fminf(s, a.most_scale) * scale, 1.4e-45f);
             } else {
                 scales[buf][1][tid - 4] = (float)e;
                 const int back = 127 + (int)(kSum - kLift) - e;
@@ -1235,6 +1238,7 @@ hipError_t launch_kv_attend(const KvAttendArgs &k, hipStream_t s)
     few.causal = k.causal;
     const float scale = k.scale != 0.0f ? k.scale : 1.0f / sqrtf((float)c.dim);
     few.scale = scale * 1.44269504088896341f;
+    few.most_scale = 0x1p127f / fabsf(few.scale);
     few.out = k.out;
     few.lse = k.lse;
     uint8_t *const ws = static_cast<uint8_t *>(k.ws);

@@ -180,3 +180,25 @@ def test_many_rows_of_the_largest_values():
         _, vcodes, _, _ = kc.split_page(pool, 1, 64, 64)
         vcodes[:] = 127
         check(pool, table, lens, news, one_hot(sum(news), 2, 64), 1, 64, kc.INT8, (120, 120), True, 1.0)
+
+
+def random_case(rng, lens, news, tokens, dim, codes, exps, q_scale, extra=1):
+    npages = sum(kc.columns(n, tokens) for n in lens) + 1
+    pool = random_pool(rng, npages, 1, tokens, dim, codes, exps)
+    table = make_table(rng, lens, tokens, npages, extra)
+    return pool, table, rng.standard_normal((sum(news), 2, dim)).astype(np.float32) * np.float32(q_scale)
+
+
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+@pytest.mark.parametrize("lens,news,extra", MANY + [([700, 500], [3, 2], 2)])
+def test_keys_and_factors_at_their_ends(codes, lens, news, extra):
+    # K scale times factor past f32's largest number, under queries of zero; and
+    # below its least normal one, under queries that would make the difference count.
+    rng = np.random.default_rng(9)
+    pool, table, q = random_case(rng, lens, news, 32, 64, codes, (-7, -4), 0.0, extra)
+    ks = kc.split_page(pool, 1, 32, 64)[2]
+    ks[:] = 2.0 ** 119
+    check(pool, table, lens, news, q, 1, 32, codes, (-7, -4), True, 2.0 ** 10)
+    q = q + rng.standard_normal(q.shape).astype(np.float32) * np.float32(2.0 ** 108)
+    ks[:] = 2.0 ** -64
+    check(pool, table, lens, news, q, 1, 32, codes, (-7, -4), True, 2.0 ** -80)
