@@ -202,3 +202,33 @@ def test_keys_and_factors_at_their_ends(codes, lens, news, extra):
     q = q + rng.standard_normal(q.shape).astype(np.float32) * np.float32(2.0 ** 108)
     ks[:] = 2.0 ** -64
     check(pool, table, lens, news, q, 1, 32, codes, (-7, -4), True, 2.0 ** -80)
+
+
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+@pytest.mark.parametrize("lens,news,extra", MANY + [([700, 500], [3, 2], 2)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_scales_far_apart(codes, lens, news, extra, dim):
+    # Scales over 2^-64..2^3 under flat and peaked scores, all small, all large;
+    # and scales that lie far apart from some tile on only.
+    say(f"far apart {codes} {news} {dim}")
+    rng = np.random.default_rng(dim)
+    for exps, q_scale in (((-64, 3), 0.05), ((-64, 3), 1.0), ((-64, -50), 1.0), ((41, 60), 2.0 ** -56)):
+        pool, table, q = random_case(rng, lens, news, 32, dim, codes, exps, q_scale, extra)
+        check(pool, table, lens, news, q, 1, 32, codes, exps)
+    pool, table, q = random_case(rng, lens, news, 32, dim, codes, (-8, -4), 1.0, extra)
+    _, _, ks, vs = kc.split_page(pool, 1, 32, dim)
+    for b, n in enumerate(lens):
+        for t in range(n * 2 // 3 // 16 * 16, n, 16):
+            vs[table[b, t // 32], 0, t % 32 // 16] = 2.0 ** rng.integers(-64, 60)
+    check(pool, table, lens, news, q, 1, 32, codes, (-64, 60))
+
+
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+@pytest.mark.parametrize("lens,news,extra", MANY + [([700, 500], [3, 2], 2)])
+@pytest.mark.parametrize("scale", [-0.3, -1e-5, 1e-6, 2.0])
+def test_factors(codes, lens, news, extra, scale):
+    say(f"factor {scale} {codes} {news}")
+    rng = np.random.default_rng(7)
+    for dim, causal in ((64, True), (128, False), (256, True)):
+        pool, table, q = random_case(rng, lens, news, 32, dim, codes, (-7, -4), 1.0, extra)
+        check(pool, table, lens, news, q, 1, 32, codes, (-7, -4), causal, scale)
