@@ -712,7 +712,9 @@ int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_to
  *   q          [total][heads][dim] of `type` (bf16 or fp16), strides in
  *              elements; base 16-byte aligned, strides multiples of 8
  *   heads      a multiple of kv_heads
- *   scale      factor of the scores; 0 means 1 / sqrt(dim)
+ *   scale      factor of the scores; 0 means 1 / sqrt(dim). At most 2.3e38 in size
+ *              (-EINVAL). A score past f32's range, and one that is not 0 under a
+ *              K scale whose product with the factor passes it, is unspecified
  *   out        [total][heads][dim] of `type`, contiguous, 16-byte aligned
  *   lse        f32[total][heads] or NULL
  *   q_start, total   as dmadesc_kv_append (total * heads < 2^31)

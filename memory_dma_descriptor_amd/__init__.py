@@ -37,6 +37,7 @@ OP_KV_RESERVE, OP_KV_COMPACT = 7, 8
 KV_E4M3, KV_INT8 = 0, 1
 KV_OK, KV_EINVAL, KV_EPAGE, KV_ENOSPC = 0, 1, 2, 3
 KV_CAUSAL = 1
+_KV_MAX_SCALE = 2.3e38           # times log2(e) still a float32
 REG_MAX_BATCH, REG_MAX_CAPACITY = 65536, 1 << 24
 REG_INVALID, REG_HIT, REG_NEW, REG_HIT_NEW, REG_NOSPACE = 0, 1, 2, 3, 4
 DEREG_OK, DEREG_REMOVED, DEREG_STALE = 0, 1, 2
@@ -757,8 +758,13 @@ def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table:
     dict(out, lse): out as q, lse f32[total, heads]. scale None means
     1 / sqrt(dim). check=True first checks the table (kv_check), synchronizes
     and raises DmadescRefused if a request names a bad page or length."""
-    if scale == 0:
-        raise ValueError("scale 0 would attend to all tokens alike; None means 1 / sqrt(dim)")
+    if scale is not None:
+        in_f32 = ctypes.c_float(scale).value
+        if in_f32 == 0:
+            raise ValueError(f"scale {scale} is 0 in float32 and would attend to all tokens alike; "
+                             "None means 1 / sqrt(dim)")
+        if not abs(in_f32) <= _KV_MAX_SCALE:
+            raise ValueError(f"scale {scale}: more than {_KV_MAX_SCALE}")
     total, heads, dim = q.shape
     dev = q.device
     cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes)

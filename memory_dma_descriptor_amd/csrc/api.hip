@@ -2,6 +2,7 @@
 // and kernel launches. Every check here runs on the host before anything is
 // launched, so a rejected call touches no memory and needs no GPU.
 #include <errno.h>
+#include <math.h>
 
 #include <atomic>
 
@@ -75,6 +76,7 @@ int build_prp_common(const uint64_t *lut, uint64_t lut_entries, const uint64_t *
 }
 
 constexpr uint64_t kMaxPages = 1ull << 31;       // page ids are i32
+constexpr float kMaxScale = 2.3e38f;             // times log2(e) still a float
 
 bool kv_sizes_ok(uint32_t kv_heads, uint32_t page_tokens, uint32_t dim)
 {
@@ -433,7 +435,7 @@ int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_to
 {
     if (!kv_cache_ok(cache) || total >= (1ull << 31) || (flags & ~DMADESC_KV_CAUSAL)) return -EINVAL;
     if (type > DMADESC_KV_FP16 || heads == 0 || heads % cache->kv_heads) return -EINVAL;
-    if (total * heads >= (1ull << 31) || !(scale == scale)) return -EINVAL;
+    if (total * heads >= (1ull << 31) || !(fabsf(scale) <= kMaxScale)) return -EINVAL;
     if (total == 0 || cache->rows == 0) return 0;
     if (!q_start || !kv_rows_ok(q, q_token_stride, q_head_stride)) return -EINVAL;
     if (!out || !aligned16(out) || !aligned4(lse)) return -EINVAL;
