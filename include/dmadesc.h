@@ -687,7 +687,9 @@ int dmadesc_kv_check(const dmadesc_kv_cache *cache, const int32_t *q_start, uint
  *              between tokens and heads; dim contiguous. Base 16-byte aligned
  *              and strides multiples of 8 (-EINVAL otherwise)
  *   q_start    i32[rows + 1], q_start[0] = 0, non-decreasing, ends at total
- *   total      new tokens of all requests, < 2^31
+ *   total      new tokens of all requests, < 2^31. A call is one launch of 2^24 - 1
+ *              workgroups at most: kv_heads * (total / 16 + 2 rows) < 2^25 - 1
+ *              (-EINVAL otherwise)
  */
 int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_token_stride,
                       int64_t k_head_stride, const void *v, int64_t v_token_stride,
@@ -717,7 +719,10 @@ int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_to
  *              K scale whose product with the factor passes it, is unspecified
  *   out        [total][heads][dim] of `type`, contiguous, 16-byte aligned
  *   lse        f32[total][heads] or NULL
- *   q_start, total   as dmadesc_kv_append (total * heads < 2^31)
+ *   q_start, total   as dmadesc_kv_append. total * heads < 2^31; calls with
+ *              heads * total / 16 + kv_heads * rows < 2^24 - 2^11 are taken, larger
+ *              ones where their launches hold 2^24 - 1 workgroups at most (-EINVAL
+ *              otherwise, and 0 bytes of workspace)
  * Workspace: dmadesc_kv_attend_workspace_bytes(...), for the partial results
  * of requests whose cache is split over several workgroups (0 bytes where the
  * table is too narrow for that; ws may then be NULL).

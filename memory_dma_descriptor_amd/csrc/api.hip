@@ -411,6 +411,7 @@ int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_to
     if (!q_start || !kv_rows_ok(k, k_token_stride, k_head_stride) ||
         !kv_rows_ok(v, v_token_stride, v_head_stride))
         return -EINVAL;
+    if (dd::kv_append_groups(total, cache->rows, cache->kv_heads) > dd::kKvMaxGroups) return -EINVAL;
     if (cache->npages == 0 || cache->width == 0) return 0;        // no page to write
     dd::KvAppendArgs a{*cache, k, v, k_token_stride, k_head_stride, v_token_stride,
                        v_head_stride, q_start, total, type};
@@ -440,6 +441,8 @@ int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_to
     if (!q_start || !kv_rows_ok(q, q_token_stride, q_head_stride)) return -EINVAL;
     if (!out || !aligned16(out) || !aligned4(lse)) return -EINVAL;
     const uint64_t tokens = (uint64_t)cache->width * cache->page_tokens;
+    if (!dd::kv_attend_fits(total, cache->rows, heads, cache->kv_heads, cache->dim, tokens))
+        return -EINVAL;
     const size_t need = dd::ws_kv_attend(total, cache->rows, heads, cache->kv_heads, cache->dim,
                                          tokens);
     if (need > 0 && !ws_ok(ws, ws_bytes, need)) return -EINVAL;

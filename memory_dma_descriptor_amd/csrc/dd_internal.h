@@ -162,6 +162,9 @@ inline uint64_t kv_page_bytes(uint64_t heads, uint64_t tokens, uint64_t dim)
     return (2 * heads * tokens * dim + 8 * heads * (tokens / 16) + 511) & ~511ull;
 }
 KvView kv_view(const dmadesc_kv_cache &c);
+// Most workgroups of 256 threads a launch holds: its threads are counted in 32 bits.
+constexpr uint64_t kKvMaxGroups = (1ull << 24) - 1;
+uint64_t kv_append_groups(uint64_t total, uint32_t rows, uint32_t kv_heads);
 hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s);
 hipError_t launch_kv_attend(const KvAttendArgs &a, hipStream_t s);
 hipError_t launch_kv_check(const dmadesc_kv_cache &c, const int32_t *q_start, uint64_t total,
@@ -177,6 +180,9 @@ hipError_t launch_kv_compact(const KvPageArgs &k, int32_t *src, int32_t *dst, in
 hipError_t launch_kv_copy(void *pool, uint64_t npages, uint64_t page_bytes, const int32_t *src,
                           const int32_t *dst, uint64_t n, const int32_t *count, hipStream_t s);
 
+// False: some launch of the call would pass kKvMaxGroups.
+bool kv_attend_fits(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads, uint32_t dim,
+                    uint64_t tokens);
 size_t ws_kv_attend(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads,
                     uint32_t dim, uint64_t tokens);
 size_t ws_kv_reserve(uint64_t npages, uint64_t n);

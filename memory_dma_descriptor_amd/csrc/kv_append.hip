@@ -280,11 +280,16 @@ void launch_type(const AppendArgs &a, uint32_t type, uint32_t codes, uint32_t gr
 
 }  // namespace
 
+uint64_t kv_append_groups(uint64_t total, uint32_t rows, uint32_t kv_heads)
+{
+    return ((total / kBlock + 2ull * rows) * 2 * kv_heads + 3) / 4;
+}
+
 hipError_t launch_kv_append(const KvAppendArgs &k, hipStream_t s)
 {
     AppendArgs a{kv_view(k.cache), k.k, k.v, k.k_tok, k.k_head, k.v_tok, k.v_head, k.q_start,
                  (uint32_t)k.total, (uint32_t)(k.total / kBlock + 2ull * k.cache.rows)};
-    const uint32_t grid = (uint32_t)(((uint64_t)a.items * 2 * k.cache.kv_heads + 3) / 4);
+    const uint32_t grid = (uint32_t)kv_append_groups(k.total, k.cache.rows, k.cache.kv_heads);
     if (k.cache.dim == 64) launch_type<64>(a, k.type, k.cache.codes, grid, s);
     else if (k.cache.dim == 128) launch_type<128>(a, k.type, k.cache.codes, grid, s);
     else launch_type<256>(a, k.type, k.cache.codes, grid, s);

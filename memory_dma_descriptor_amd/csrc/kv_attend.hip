@@ -1147,6 +1147,7 @@ struct Launch {
     uint32_t most;               // rows of a request up to which it is the first kernel's
     uint32_t join;               // workgroups of the join, 0: nothing can be split
     size_t plan_at, few_lse, few_part, many_lse, many_part, bytes;
+    bool fits;                   // false: too many workgroups for a launch, the rest is not set
 };
 
 Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads, uint32_t dim,
@@ -1164,19 +1165,24 @@ Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_head
     // more of each request at most.
     const uint64_t few_rows = both && all > rows * (uint64_t)kMostFew ? rows * (uint64_t)kMostFew : all;
     const uint64_t big = both ? all / (kMostFew + 1) : rows;      // requests that have many
-    auto grid = [&](uint64_t base, bool split, uint32_t slots, uint32_t long_) -> uint32_t {
-        if (!split) return (uint32_t)base;
+    auto grid = [&](uint64_t base, bool split, uint32_t slots, uint32_t long_) -> uint64_t {
+        if (!split || base > kKvMaxGroups) return base;
         const uint32_t one = most_pieces((uint32_t)base, slots), two = most_pieces((uint32_t)base, 2 * slots);
         return base * tiles > (uint64_t)long_ * slots / 4 && two > one ? two : one;
     };
+    uint64_t n_few = 0, n_many = 0, n_join = 0;
     if (few)
-        p.few = grid(kv_heads * (few_rows / p.tile_rows + rows), split_few,
+        n_few = grid(kv_heads * (few_rows / p.tile_rows + rows), split_few,
                      slots_few((int)dim, (int)p.tile_rows / 16), kLongFew);
     if (!few || both)
-        p.many = grid(kv_heads * (all / kRowsMany + (big < rows ? big : rows)), split_many,
+        n_many = grid(kv_heads * (all / kRowsMany + (big < rows ? big : rows)), split_many,
                       slots_many((int)dim), kLongMany);
-    if ((p.few && split_few) || (p.many && split_many))
-        p.join = (uint32_t)(kv_heads * (all / kJoinRows + rows));
+    if ((n_few && split_few) || (n_many && split_many)) n_join = kv_heads * (all / kJoinRows + rows);
+    p.fits = n_few <= kKvMaxGroups && n_many <= kKvMaxGroups && n_join <= kKvMaxGroups;
+    if (!p.fits) return p;
+    p.few = (uint32_t)n_few;
+    p.many = (uint32_t)n_many;
+    p.join = (uint32_t)n_join;
     size_t at = align256(8ull * rows);
     auto take = [&](size_t bytes) { const size_t r = at; at += align256(bytes); return r; };
     const size_t f = split_few ? p.few : 0, n = split_many ? p.many : 0;
@@ -1217,6 +1223,12 @@ void launch_dim(const KvAttendArgs &k, const AttendArgs &few, const AttendArgs &
 }
 
 }  // namespace
+
+bool kv_attend_fits(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads, uint32_t dim,
+                    uint64_t tokens)
+{
+    return launch_of(total, rows, heads, kv_heads, dim, tokens).fits;
+}
 
 size_t ws_kv_attend(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads,
                     uint32_t dim, uint64_t tokens)

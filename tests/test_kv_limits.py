@@ -41,3 +41,37 @@ def test_binding_refuses_factors_that_f32_cannot_hold(scale):
     q = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="scale"):
         dd.kv_attend(q, None, None, None, None, 2, 16, scale=scale)
+
+
+@no_gpu_only
+def test_append_sizes_past_a_launch():
+    # A launch holds 2^24 - 1 workgroups of 256 threads; four waves of one share a
+    # workgroup, two for each block of 16 tokens and head.
+    f = dd.lib().dmadesc_kv_append
+
+    def append(rows, heads, total):
+        return f(cache(rows=rows, kv_heads=heads, page_tokens=16), P, 8, 8, P, 8, 8, P, total, 0, None)
+
+    top = (1 << 24) - 1
+    for bad in ((top, 1024, 1), (top, 256, 1), (1 << 22, 8, 1), (1 << 22, 1024, 16), (1, 1024, 1 << 30),
+                (1 << 23, 2, 16)):
+        assert append(*bad) == EINVAL, bad
+    for good in ((1 << 22, 3, 1), (1, 1024, 1 << 18), ((1 << 23) - 1, 2, 15)):
+        assert append(*good) not in (0, EINVAL), good      # gets as far as a launch
+
+
+@no_gpu_only
+def test_attend_sizes_past_a_launch():
+    size = dd.lib().dmadesc_kv_attend_workspace_bytes
+    # rows, heads = kv_heads, total, width in pages of 16 tokens (256 are split, 8 not)
+    for rows, heads, total, width in (((1 << 24) - 1, 1024, 16, 256), ((1 << 24) - 1, 256, 1, 256),
+                                      (3 << 20, 8, 16, 256), (1 << 22, 1024, 16, 256),
+                                      (1, 64, 1 << 24, 256)):
+        assert size(total, rows, heads, heads, 64, width, 16) == 0
+        for w in (width, 8) if rows > 1 else (width,):
+            assert attend(cache(rows=rows, kv_heads=heads, page_tokens=16, width=w), total, heads) == EINVAL
+    for rows, heads, total, width in ((1 << 20, 8, 16, 256), (1, 64, 1 << 20, 256),
+                                      (1, 64, 1 << 24, 8)):
+        assert (size(total, rows, heads, heads, 64, width, 16) > 0) == (width > 16)
+        assert attend(cache(rows=rows, kv_heads=heads, page_tokens=16, width=width), total, heads) \
+            not in (0, EINVAL)
