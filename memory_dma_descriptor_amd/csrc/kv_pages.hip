@@ -152,7 +152,7 @@ struct ReserveArgs {
     uint8_t *free_bits;        // [page chunks][256] which of a thread's 8 pages are free, on entry
     uint64_t *slot_sum;        // [slot chunks] pages taken
     uint32_t *take;            // [n] pages taken; bit 31: the last page is copied; kNone: refused
-    uint32_t *upto;            // [n] pages taken by the chunk's slots up to this one
+    uint64_t *upto;            // [n] pages taken by the chunk's slots up to this one
     uint32_t *from;            // [n] first table column the slot writes
 };
 
@@ -211,6 +211,7 @@ __device__ __forceinline__ T block_sum(T v, T *scratch)
 __global__ __launch_bounds__(kThreads) void k_reserve_count(ReserveArgs a)
 {
     __shared__ uint32_t scratch[kThreads / kWave];
+    __shared__ uint64_t sums[kThreads / kWave];
     if (blockIdx.x < a.page_chunks) {
         const uint32_t f = page_flags(a.t, blockIdx.x, [](uint32_t, int32_t r) { return r == 0; });
         const uint32_t s = block_sum<uint32_t>(__popc(f), scratch);
@@ -221,8 +222,9 @@ __global__ __launch_bounds__(kThreads) void k_reserve_count(ReserveArgs a)
     const uint32_t chunk = blockIdx.x - a.page_chunks, i = chunk * kThreads + threadIdx.x;
     uint32_t take = 0, from = 0;
     if (i < a.n) take = slot_take(a, i, from);
-    uint32_t all;
-    const uint32_t before = block_excl_scan<kThreads, uint32_t>(taken(take), scratch, &all);
+    // In 64 bits: 256 slots may ask for up to 2^27 pages each.
+    uint64_t all;
+    const uint64_t before = block_excl_scan<kThreads, uint64_t>(taken(take), sums, &all);
     if (i < a.n) {
         a.take[i] = take;
         a.from[i] = from;
@@ -298,7 +300,7 @@ __global__ __launch_bounds__(kThreads) void k_reserve_give(ReserveArgs a)
                 else lo = mid + 1;
             }
             const uint64_t first = lo ? sums[lo - 1] : start;
-            const uint32_t in = (uint32_t)(mine - first);
+            const uint64_t in = mine - first;
             // First slot of it with upto > in: of 16 groups of 16, then of 16 slots, so
             // that there are two waits and not eight.
             const uint32_t s0 = (c0 + lo) * kThreads, last_slot = a.n - 1;
@@ -313,9 +315,10 @@ __global__ __launch_bounds__(kThreads) void k_reserve_give(ReserveArgs a)
                 }
                 x += below * step;
             }
-            const uint32_t v = a.take[x], upto = a.upto[x];
+            const uint32_t v = a.take[x];
+            const uint64_t upto = a.upto[x];
             if (first + upto > nfree) continue;     // the slot is refused: out of pages
-            const uint32_t at = in - (upto - taken(v));
+            const uint32_t at = (uint32_t)(in - (upto - taken(v)));
             const uint32_t page = chunk * kChunk + order[mine - before];
             int32_t *const entry = t.table + (uint64_t)(uint32_t)a.slot[x] * t.width + a.from[x] + at;
             if (at == 0 && (v & kShared)) {
@@ -498,7 +501,7 @@ size_t ws_kv_reserve(uint64_t npages, uint64_t n)
 {
     const uint32_t pc = chunks_of(npages, kChunk);
     return align256(4ull * pc) + align256((size_t)kThreads * pc) +
-           align256(8ull * chunks_of(n, kThreads)) + 3 * align256(4ull * n);
+           align256(8ull * chunks_of(n, kThreads)) + 2 * align256(4ull * n) + align256(8ull * n);
 }
 
 hipError_t launch_kv_reserve(const KvPageArgs &k, const int32_t *slot, const int32_t *n_new,
@@ -513,7 +516,7 @@ hipError_t launch_kv_reserve(const KvPageArgs &k, const int32_t *slot, const int
     a.free_bits = take((size_t)kThreads * pc);
     a.slot_sum = reinterpret_cast<uint64_t *>(take(8ull * sc));
     a.take = reinterpret_cast<uint32_t *>(take(4ull * k.n));
-    a.upto = reinterpret_cast<uint32_t *>(take(4ull * k.n));
+    a.upto = reinterpret_cast<uint64_t *>(take(8ull * k.n));
     a.from = reinterpret_cast<uint32_t *>(take(4ull * k.n));
     k_reserve_count<<<pc + sc, kThreads, 0, s>>>(a);
     k_reserve_give<<<pc + sc, kThreads, 0, s>>>(a);

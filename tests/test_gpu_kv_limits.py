@@ -232,3 +232,18 @@ def test_factors(codes, lens, news, extra, scale):
     for dim, causal in ((64, True), (128, False), (256, True)):
         pool, table, q = random_case(rng, lens, news, 32, dim, codes, (-7, -4), 1.0, extra)
         check(pool, table, lens, news, q, 1, 32, codes, (-7, -4), causal, scale)
+
+
+def test_reserve_more_pages_than_32_bits_count():
+    # 128 slots of one call ask for 2^25 pages each, 2^32 with the single pages of the
+    # first and the last one: only the first can have its page.
+    rows, width, tokens = 130, 1 << 25, 16
+    table = torch.empty((rows, width), dtype=torch.int32, device="cuda")     # 17 GiB, not read
+    table[:, 0] = -1
+    refs, lens = torch.zeros(300, dtype=torch.int32, device="cuda"), i32([0] * rows)
+    news = [16] + [width * tokens] * 128 + [16]
+    r = dd.kv_reserve(refs, table, lens, i32(range(rows)), i32(news), tokens, check=False)
+    assert r["status"].tolist() == [dd.KV_OK] + [dd.KV_ENOSPC] * 129
+    assert lens.tolist() == [16] + [0] * 129 and refs.tolist() == [1] + [0] * 299
+    assert table[:, 0].tolist() == [0] + [-1] * 129
+    assert (r["src"] == -1).all() and (r["dst"] == -1).all()
