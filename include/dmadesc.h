@@ -742,7 +742,9 @@ size_t dmadesc_kv_attend_workspace_bytes(uint64_t total, uint32_t rows, uint32_t
  * A row of n tokens holds the pages of its first ceil(n / page_tokens) table
  * entries. The listed rows of one call are distinct, and no row is both
  * parent and child (otherwise the result is unspecified but memory-safe).
- * status u8[n] (enum dmadesc_kv_status): a refused row is left as it was.
+ * status u8[n] (enum dmadesc_kv_status): a refused row is left as it was. Table
+ * entries outside the pool are otherwise passed over: they have no references to
+ * drop or to gain.
  *
  * dmadesc_kv_free: cuts row[i] to its first keep[i] tokens (keep NULL: none),
  * dropping a reference of every page past them and setting all further table
@@ -756,7 +758,8 @@ size_t dmadesc_kv_attend_workspace_bytes(uint64_t total, uint32_t rows, uint32_t
  * for each page the longer row needs and one in place of a partly filled last
  * page that is shared (refs > 1 on entry): src[i] is then that page, dst[i] the
  * one to copy it to, otherwise both are -1. A slot for which the pages run
- * out, counting those of all slots before it, is refused with ENOSPC.
+ * out, counting those of all slots before it, is refused with ENOSPC, one whose
+ * partly filled last page is outside the pool with EPAGE.
  *   Workspace: dmadesc_workspace_bytes(DMADESC_OP_KV_RESERVE, npages, n).
  *
  * dmadesc_kv_compact: with L live pages (refs > 0), the live pages at or past L

@@ -843,7 +843,7 @@ def kv_reserve(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, slot
     """Extends rows slot[i] by n_new[i] tokens with free pages; returns dict(src,
     dst, status): pages to copy with kv_copy_pages, -1 where there is none.
     check=True synchronizes and raises DmadescRefused for refused rows (KV_ENOSPC:
-    the free pages ran out)."""
+    the free pages ran out; KV_EPAGE: its partly filled last page is outside the pool)."""
     n = slot.numel()
     dev = refs.device
     out = dict(src=_kv_new(n, torch.int32, dev, stream), dst=_kv_new(n, torch.int32, dev, stream),

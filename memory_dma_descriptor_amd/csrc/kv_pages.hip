@@ -151,17 +151,17 @@ struct ReserveArgs {
     uint32_t *free_count;      // [page chunks] free pages
     uint8_t *free_bits;        // [page chunks][256] which of a thread's 8 pages are free, on entry
     uint64_t *slot_sum;        // [slot chunks] pages taken
-    uint32_t *take;            // [n] pages taken; bit 31: the last page is copied; kNone: refused
+    uint32_t *take;            // [n] pages taken; bit 31: the last page is copied; kNone, kBadPage: refused
     uint64_t *upto;            // [n] pages taken by the chunk's slots up to this one
     uint32_t *from;            // [n] first table column the slot writes
 };
 
-constexpr uint32_t kShared = 1u << 31;
+constexpr uint32_t kShared = 1u << 31, kBadPage = kNone - 1;
 
-__device__ __forceinline__ uint32_t taken(uint32_t take) { return take == kNone ? 0u : take & ~kShared; }
+__device__ __forceinline__ uint32_t taken(uint32_t take) { return take >= kBadPage ? 0u : take & ~kShared; }
 
 // What slot i needs: its pages, whether its last page is shared and partly
-// filled; kNone where the slot is refused.
+// filled; kNone where the slot is refused, kBadPage where it is for that page.
 __device__ __forceinline__ uint32_t slot_take(const ReserveArgs &a, uint32_t i, uint32_t &from)
 {
     const Table &t = a.t;
@@ -176,7 +176,7 @@ __device__ __forceinline__ uint32_t slot_take(const ReserveArgs &a, uint32_t i, 
     bool shared = false;
     if (len & ((1 << t.tshift) - 1)) {
         const int32_t last = t.table[(uint64_t)r * t.width + have - 1];
-        if (!page_ok(t, last)) return kNone;
+        if (!page_ok(t, last)) return kBadPage;
         shared = t.refs[last] > 1;
     }
     from = have - (shared ? 1u : 0u);
@@ -259,9 +259,13 @@ __global__ __launch_bounds__(kThreads) void k_reserve_give(ReserveArgs a)
         if (i >= a.n) return;
         const uint32_t v = a.take[i];
         const bool full = taken(v) > 0 && first + a.upto[i] > nfree;
-        if (v == kNone || full || !(v & kShared)) a.src[i] = a.dst[i] = -1;
-        a.status[i] = v == kNone ? DMADESC_KV_EINVAL : full ? DMADESC_KV_ENOSPC : DMADESC_KV_OK;
-        if (v != kNone && !full) t.lens[a.slot[i]] += a.n_new[i];
+        const bool refused = v >= kBadPage;
+        if (refused || full || !(v & kShared)) a.src[i] = a.dst[i] = -1;
+        a.status[i] = v == kNone      ? DMADESC_KV_EINVAL
+                      : v == kBadPage ? DMADESC_KV_EPAGE
+                      : full          ? DMADESC_KV_ENOSPC
+                                      : DMADESC_KV_OK;
+        if (!refused && !full) t.lens[a.slot[i]] += a.n_new[i];
         return;
     }
     before = block_sum(before, scratch);

@@ -247,3 +247,14 @@ def test_reserve_more_pages_than_32_bits_count():
     assert lens.tolist() == [16] + [0] * 129 and refs.tolist() == [1] + [0] * 299
     assert table[:, 0].tolist() == [0] + [-1] * 129
     assert (r["src"] == -1).all() and (r["dst"] == -1).all()
+
+
+def test_reserve_names_bad_pages():
+    # A partly filled last page outside the pool; the same entry under a full page
+    # and in a row that takes nothing is not looked at.
+    state = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (
+        [1, 0, 0, 0], [[9, -1], [-1, -1], [-7, -1], [5, -1], [9, -1], [0, -1]], [3, 16, 1, 16, 3, 4])]
+    r = dd.kv_reserve(*state, i32(range(6)), i32([1, 1, 40, 1, 0, 13]), 16, check=False)
+    assert r["status"].tolist() == [dd.KV_EPAGE, dd.KV_OK, dd.KV_EINVAL, dd.KV_OK, dd.KV_OK, dd.KV_OK]
+    assert state[2].tolist() == [3, 17, 1, 17, 3, 17] and state[0].tolist() == [1, 1, 1, 1]
+    assert state[1].tolist() == [[9, -1], [-1, 1], [-7, -1], [5, 2], [9, -1], [0, 3]]
