@@ -523,7 +523,8 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
 
             const int tok = t * kTile + g * kBlock;       // first token of the lane's block
             const bool edge = t * kTile + kTile - 1 > low;   // some row does not see the whole tile
-            const float ve = (float)((int)(__float_as_uint(vscale) >> 23 & 0xffu) - 126);
+            // (A scale of 0, of a page that was never written, stands for codes of 0.)
+            const float ve = fmaxf((float)((int)(__float_as_uint(vscale) >> 23 & 0xffu) - 126), kMinExp + 1.0f);
             f16x8 pf[kNt][2];
 #pragma unroll
             for (int n = 0; n < kNt; ++n) {
@@ -860,14 +861,14 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     auto stage_scales = [&](int t, int buf) {
         if (tid < 8) {                              // K: scale; V: exponent and 2^-exponent
             const float s = (t * 4 + (tid & 3)) * kBlock < len ? sc : 1.0f;
-            const int e = (int)(__float_as_uint(s) >> 23 & 0xffu) - 127;
+            // (A scale of 0, of a page that was never written, stands for codes of 0.)
+            const int eb = (int)(__float_as_uint(s) >> 23 & 0xffu) - 127, e = eb < kMinExp ? kMinExp : eb;
             if (tid < 4) {
                 // Never 0, so that a masked -inf stays one, and finite, so that a 0 does.
                 scales[buf][0][tid] = fmaxf(fminf(s, a.most_scale) * scale, 1.4e-45f);
             } else {
                 scales[buf][1][tid - 4] = (float)e;
-                const int back = 127 + (int)(kSum - kLift) - e;
-                scales[buf][2][tid - 4] = __uint_as_float((uint32_t)(back < 254 ? back : 254) << 23);
+                scales[buf][2][tid - 4] = __uint_as_float((uint32_t)(127 + (int)(kSum - kLift) - e) << 23);
             }
         }
     };

@@ -234,6 +234,20 @@ def test_factors(codes, lens, news, extra, scale):
         check(pool, table, lens, news, q, 1, 32, codes, (-7, -4), causal, scale)
 
 
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+@pytest.mark.parametrize("lens,news,extra", MANY + [([700, 500], [3, 2], 2), ([100, 5], [3, 9], 2)])
+def test_pages_never_written(codes, lens, news, extra):
+    # Scales of 0 under codes of 0, as a zeroed pool has them, alone and beside others.
+    rng = np.random.default_rng(11)
+    pool, table, q = random_case(rng, lens, news, 32, 64, codes, (-7, -4), 1.0, extra)
+    _, vcodes, ks, vs = kc.split_page(pool, 1, 32, 64)
+    for p in range(0, len(pool), 3):
+        ks[p], vs[p], vcodes[p] = 0, 0, 0
+    check(pool, table, lens, news, q, 1, 32, codes, (-127, -4))
+    pool[:] = 0
+    check(pool, table, lens, news, q, 1, 32, codes, (-127, -4))
+
+
 def test_reserve_more_pages_than_32_bits_count():
     # 128 slots of one call ask for 2^25 pages each, 2^32 with the single pages of the
     # first and the last one: only the first can have its page.
