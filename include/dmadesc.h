@@ -624,8 +624,9 @@ int dmadesc_reg_deregister(uint64_t *start, uint64_t *end, uint64_t *id, uint32_
  *   V scales  f32[H][T/16]
  * padded to a multiple of 512 bytes (dmadesc_kv_page_bytes). A value is its
  * code times the scale of its block of 16 tokens and one head; scales are
- * powers of two, 2^-64 or more (0 in a page of zeros, whose values are 0). Page p lies at pool + p * page bytes. Token t
- * of request r lies in page table[r * width + t / T].
+ * powers of two, 2^-64 or more (0 in a page of zeros, whose values are 0).
+ * Page p lies at pool + p * page bytes. Token t of request r lies in page
+ * table[r * width + t / T].
  *   pool         u8[npages][page bytes], 16-byte aligned
  *   table        i32[rows][width] pages of each request; entries past the
  *                length are not read

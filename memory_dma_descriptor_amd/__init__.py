@@ -189,6 +189,20 @@ def workspace_bytes(op: int, n: int, param: int = 0) -> int:
     return int(lib().dmadesc_workspace_bytes(op, n, param))
 
 
+def _new(size, dtype, device, stream) -> torch.Tensor:
+    """A device tensor that a call on `stream` (None: the current one) fills. It
+    is taken in that stream's order: memory of the current stream may have been
+    freed while work queued there still uses it, which `stream` does not wait
+    for. The current stream is noted as a user, so that the memory is not handed
+    out again under what the caller does with the result there."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(size, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _workspace(op: int, n: int, param: int, device, ws):
     """(tensor, pointer, bytes) of a device workspace for `op`: the caller's
     `ws` (a contiguous uint8 device tensor, checked) or a new one."""
@@ -669,15 +683,6 @@ def _kv_page_bytes(kv_heads, page_tokens, dim):
     return kv_page_bytes(kv_heads, page_tokens, dim)
 
 
-def _kv_new(size, dtype, device, stream):
-    """A device tensor the call fills on `stream` (which may not be the
-    current one: the allocator must not hand the memory out before it is done)."""
-    t = torch.empty(size, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes):
     if table.dim() != 2 or pool.dim() != 2:
         raise ValueError("pool must be u8[npages, page_bytes] and table i32[rows, width]")
@@ -722,7 +727,7 @@ def kv_check(q_start: torch.Tensor | None, total: int, pool: torch.Tensor, table
     """Status u8[rows] (KV_OK, KV_EINVAL, KV_EPAGE) of a cache's table, lengths
     and, unless None, q_start (dmadesc_kv_check)."""
     cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, 0)
-    status = _kv_new(table.shape[0], torch.uint8, pool.device, stream)
+    status = _new(table.shape[0], torch.uint8, pool.device, stream)
     q = None if q_start is None else _dev(q_start, torch.int32, "q_start", table.shape[0] + 1)
     rc = lib().dmadesc_kv_check(ctypes.byref(cache), q, total, appending, status.data_ptr(),
                                 _stream(pool.device, stream))
@@ -775,12 +780,12 @@ def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table:
                           stream)
         _kv_refused("dmadesc_kv_attend", status, stream, dict(status=status))
     if out is None:
-        out = dict(out=_kv_new((total, heads, dim), q.dtype, dev, stream),
-                   lse=_kv_new((total, heads), torch.float32, dev, stream))
+        out = dict(out=_new((total, heads, dim), q.dtype, dev, stream),
+                   lse=_new((total, heads), torch.float32, dev, stream))
     if ws is None:
         rows, width = table.shape
         need = _kv_attend_bytes(total, rows, heads, kv_heads, dim, width, page_tokens)
-        ws = _kv_new(need, torch.uint8, dev, stream) if need else None
+        ws = _new(need, torch.uint8, dev, stream) if need else None
     ws_bytes = 0 if ws is None else ws.numel()
     rc = lib().dmadesc_kv_attend(
         ctypes.byref(cache), *qp, qs, total, heads, _KV_TYPE[q.dtype],
@@ -807,7 +812,7 @@ def kv_free(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, row: to
     drops their references of the pages past them; returns dict(status).
     check=True synchronizes and raises DmadescRefused for refused rows."""
     n = row.numel()
-    status = _kv_new(n, torch.uint8, refs.device, stream)
+    status = _new(n, torch.uint8, refs.device, stream)
     k = None if keep is None else _dev(keep, torch.int32, "keep", n)
     rc = lib().dmadesc_kv_free(*_kv_state(refs, table, lens, page_tokens),
                                _dev(row, torch.int32, "row"), k, n, status.data_ptr(),
@@ -825,7 +830,7 @@ def kv_fork(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, parent:
     pages; returns dict(status). check=True synchronizes and raises
     DmadescRefused for refused rows."""
     n = parent.numel()
-    status = _kv_new(n, torch.uint8, refs.device, stream)
+    status = _new(n, torch.uint8, refs.device, stream)
     rc = lib().dmadesc_kv_fork(*_kv_state(refs, table, lens, page_tokens),
                                _dev(parent, torch.int32, "parent"),
                                _dev(child, torch.int32, "child", n), n, status.data_ptr(),
@@ -846,10 +851,10 @@ def kv_reserve(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, slot
     the free pages ran out; KV_EPAGE: its partly filled last page is outside the pool)."""
     n = slot.numel()
     dev = refs.device
-    out = dict(src=_kv_new(n, torch.int32, dev, stream), dst=_kv_new(n, torch.int32, dev, stream),
-               status=_kv_new(n, torch.uint8, dev, stream))
+    out = dict(src=_new(n, torch.int32, dev, stream), dst=_new(n, torch.int32, dev, stream),
+               status=_new(n, torch.uint8, dev, stream))
     if ws is None:
-        ws = _kv_new(workspace_bytes(OP_KV_RESERVE, refs.numel(), n), torch.uint8, dev, stream)
+        ws = _new(workspace_bytes(OP_KV_RESERVE, refs.numel(), n), torch.uint8, dev, stream)
     rc = lib().dmadesc_kv_reserve(
         *_kv_state(refs, table, lens, page_tokens), _dev(slot, torch.int32, "slot"),
         _dev(n_new, torch.int32, "n_new", n), n, out["src"].data_ptr(), out["dst"].data_ptr(),
@@ -868,11 +873,11 @@ def kv_compact(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, page
     state = _kv_state(refs, table, lens, page_tokens)
     npages = refs.numel()
     dev = refs.device
-    out = dict(src=_kv_new(npages // 2, torch.int32, dev, stream),
-               dst=_kv_new(npages // 2, torch.int32, dev, stream),
-               moves=_kv_new(1, torch.int32, dev, stream))
+    out = dict(src=_new(npages // 2, torch.int32, dev, stream),
+               dst=_new(npages // 2, torch.int32, dev, stream),
+               moves=_new(1, torch.int32, dev, stream))
     if ws is None:
-        ws = _kv_new(workspace_bytes(OP_KV_COMPACT, npages), torch.uint8, dev, stream)
+        ws = _new(workspace_bytes(OP_KV_COMPACT, npages), torch.uint8, dev, stream)
     rc = lib().dmadesc_kv_compact(state[0], npages, state[2], state[4], state[5],
                                   out["src"].data_ptr(), out["dst"].data_ptr(),
                                   out["moves"].data_ptr(), _dev(ws, torch.uint8, "ws"),
