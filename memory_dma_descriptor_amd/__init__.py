@@ -203,12 +203,12 @@ def _new(size, dtype, device, stream) -> torch.Tensor:
     return t
 
 
-def _workspace(op: int, n: int, param: int, device, ws):
+def _workspace(op: int, n: int, param: int, device, ws, stream):
     """(tensor, pointer, bytes) of a device workspace for `op`: the caller's
     `ws` (a contiguous uint8 device tensor, checked) or a new one."""
     need = workspace_bytes(op, n, param)
     if ws is None:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        ws = _new(max(need, 1), torch.uint8, device, stream)
     ptr = _dev(ws, torch.uint8, "ws")
     nbytes = ws.numel() * ws.element_size()
     if nbytes < need:
@@ -227,13 +227,13 @@ def mr_lookup(reg_start: torch.Tensor, reg_end: torch.Tensor, reg_lkey: torch.Te
     dev = off.device
     ws_ptr, ws_bytes = None, 0
     if records and workspace_bytes(OP_MR_LOOKUP, n, r) > 0:
-        ws, ws_ptr, ws_bytes = _workspace(OP_MR_LOOKUP, n, r, dev, ws)
+        ws, ws_ptr, ws_bytes = _workspace(OP_MR_LOOKUP, n, r, dev, ws, stream)
     if out is None:
-        out = dict(handle=torch.empty(n, dtype=torch.int32, device=dev),
-                   lkey=torch.empty(n, dtype=torch.uint32, device=dev),
-                   kind=torch.empty(n, dtype=torch.uint8, device=dev),
-                   rbase=torch.empty(n, dtype=torch.uint64, device=dev),
-                   rend=torch.empty(n, dtype=torch.uint64, device=dev))
+        out = dict(handle=_new(n, torch.int32, dev, stream),
+                   lkey=_new(n, torch.uint32, dev, stream),
+                   kind=_new(n, torch.uint8, dev, stream),
+                   rbase=_new(n, torch.uint64, dev, stream),
+                   rend=_new(n, torch.uint64, dev, stream))
     rc = lib().dmadesc_mr_lookup(
         _dev(reg_start, torch.uint64, "reg_start", r), _dev(reg_end, torch.uint64, "reg_end", r),
         _dev(reg_lkey, torch.uint32, "reg_lkey", r), r, page_shift,
@@ -252,7 +252,7 @@ def mr_table_check(reg_start: torch.Tensor, reg_end: torch.Tensor, page_shift: i
     synchronizes the stream)."""
     r = reg_start.numel()
     dev = reg_start.device
-    scratch = torch.empty(1, dtype=torch.uint64, device=dev)
+    scratch = _new(1, torch.uint64, dev, stream)
     bad = ctypes.c_uint64(0)
     rc = lib().dmadesc_mr_table_check(
         _dev(reg_start, torch.uint64, "reg_start", r), _dev(reg_end, torch.uint64, "reg_end", r),
@@ -284,11 +284,11 @@ def build_prp(lut: torch.Tensor, off: torch.Tensor, length: torch.Tensor,
     if pool.dim() != 2 or pool.shape[1] != 512:
         raise ValueError("pool must have shape [pool_pages, 512]")
     if out is None:
-        out = dict(prp1=torch.empty(n, dtype=torch.uint64, device=dev),
-                   prp2=torch.empty(n, dtype=torch.uint64, device=dev),
-                   status=torch.empty(n, dtype=torch.uint8, device=dev),
-                   total_pages=torch.empty(1, dtype=torch.uint64, device=dev))
-    ws = _workspace(OP_BUILD_PRP, n, 0, dev, ws)
+        out = dict(prp1=_new(n, torch.uint64, dev, stream),
+                   prp2=_new(n, torch.uint64, dev, stream),
+                   status=_new(n, torch.uint8, dev, stream),
+                   total_pages=_new(1, torch.uint64, dev, stream))
+    ws = _workspace(OP_BUILD_PRP, n, 0, dev, ws, stream)
     fn = lib().dmadesc_build_prp_packed if packed else lib().dmadesc_build_prp
     rc = fn(
         _dev(lut, torch.uint64, "lut"), lut.numel(),
@@ -346,10 +346,10 @@ def partition_by_queue(qid: torch.Tensor, nqueues: int, out: dict | None = None,
     n = qid.numel()
     dev = qid.device
     if out is None:
-        out = dict(perm=torch.empty(n, dtype=torch.uint32, device=dev),
-                   qoff=torch.empty(nqueues + 2, dtype=torch.uint64, device=dev),
-                   n_invalid=torch.empty(1, dtype=torch.uint64, device=dev))
-    ws = _workspace(OP_PARTITION, n, nqueues, dev, ws)
+        out = dict(perm=_new(n, torch.uint32, dev, stream),
+                   qoff=_new(nqueues + 2, torch.uint64, dev, stream),
+                   n_invalid=_new(1, torch.uint64, dev, stream))
+    ws = _workspace(OP_PARTITION, n, nqueues, dev, ws, stream)
     rc = lib().dmadesc_partition_by_queue(
         _dev(qid, torch.uint32, "qid", n), n, nqueues,
         _dev(out["perm"], torch.uint32, "perm", n),
@@ -390,22 +390,22 @@ def build_batch(lut: torch.Tensor, off: torch.Tensor, length: torch.Tensor,
     lookup = lookup and reg_start is not None
     r = reg_start.numel() if lookup else 0
     if out is None:
-        out = dict(prp1=torch.empty(n, dtype=torch.uint64, device=dev),
-                   prp2=torch.empty(n, dtype=torch.uint64, device=dev),
-                   status=torch.empty(n, dtype=torch.uint8, device=dev),
-                   total_pages=torch.empty(1, dtype=torch.uint64, device=dev),
-                   perm=torch.empty(n, dtype=torch.uint32, device=dev),
-                   qoff=torch.empty(nqueues + 2, dtype=torch.uint64, device=dev),
-                   n_invalid=torch.empty(1, dtype=torch.uint64, device=dev))
+        out = dict(prp1=_new(n, torch.uint64, dev, stream),
+                   prp2=_new(n, torch.uint64, dev, stream),
+                   status=_new(n, torch.uint8, dev, stream),
+                   total_pages=_new(1, torch.uint64, dev, stream),
+                   perm=_new(n, torch.uint32, dev, stream),
+                   qoff=_new(nqueues + 2, torch.uint64, dev, stream),
+                   n_invalid=_new(1, torch.uint64, dev, stream))
         if lookup:
-            out.update(handle=torch.empty(n, dtype=torch.int32, device=dev),
-                       lkey=torch.empty(n, dtype=torch.uint32, device=dev),
-                       kind=torch.empty(n, dtype=torch.uint8, device=dev),
-                       rbase=torch.empty(n, dtype=torch.uint64, device=dev),
-                       rend=torch.empty(n, dtype=torch.uint64, device=dev))
+            out.update(handle=_new(n, torch.int32, dev, stream),
+                       lkey=_new(n, torch.uint32, dev, stream),
+                       kind=_new(n, torch.uint8, dev, stream),
+                       rbase=_new(n, torch.uint64, dev, stream),
+                       rend=_new(n, torch.uint64, dev, stream))
     need = batch_workspace_bytes(n, nqueues, r)
     if ws is None:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        ws = _new(max(need, 1), torch.uint8, dev, stream)
     wptr = _dev(ws, torch.uint8, "ws")
     if ws.numel() < need:
         raise ValueError(f"workspace needs {need} bytes, got {ws.numel()}")
@@ -466,11 +466,11 @@ def emit_sqe(perm: torch.Tensor, qoff: torch.Tensor, status: torch.Tensor,
     nq = ring.numel()
     dev = status.device
     if placed is None:
-        placed = torch.empty(nq, dtype=torch.uint32, device=dev)
+        placed = _new(nq, torch.uint32, dev, stream)
     rid = 0
     if req_of_slot is not None:
         rid = _dev(req_of_slot, torch.uint32, "req_of_slot", nq * SQ_MAX_DEPTH)
-    ws = _workspace(OP_EMIT_SQE, n, nq, dev, ws)
+    ws = _workspace(OP_EMIT_SQE, n, nq, dev, ws, stream)
     rc = lib().dmadesc_emit_sqe(
         _dev(perm, torch.uint32, "perm", n), _dev(qoff, torch.uint64, "qoff", nq + 2), nq,
         _dev(status, torch.uint8, "status", n), _dev(length, torch.uint64, "len", n),
@@ -502,11 +502,11 @@ def build_put(src: torch.Tensor, dst: torch.Tensor, nbytes: torch.Tensor, pe: to
         raise ValueError("key tables smaller than the heap's chunks (lkeys[nchunks], "
                          "rkeys[npes * nchunks])")
     if out is None:
-        out = dict(first=torch.empty(n, dtype=torch.uint64, device=dev),
-                   count=torch.empty(n, dtype=torch.uint32, device=dev),
-                   status=torch.empty(n, dtype=torch.uint8, device=dev),
-                   total=torch.empty(1, dtype=torch.uint64, device=dev))
-    ws = _workspace(OP_BUILD_PUT, n, 0, dev, ws)
+        out = dict(first=_new(n, torch.uint64, dev, stream),
+                   count=_new(n, torch.uint32, dev, stream),
+                   status=_new(n, torch.uint8, dev, stream),
+                   total=_new(1, torch.uint64, dev, stream))
+    ws = _workspace(OP_BUILD_PUT, n, 0, dev, ws, stream)
     rc = lib().dmadesc_build_put(
         _dev(src, torch.uint64, "src", n), _dev(dst, torch.uint64, "dst", n),
         _dev(nbytes, torch.uint64, "bytes", n), _dev(pe, torch.uint32, "pe", n), n,
@@ -622,10 +622,10 @@ class DeviceRegistry:
         """Returns dict(handle u64[n], kind u8[n], needed)."""
         n = addr.numel()
         dev = self.device
-        handle = torch.empty(n, dtype=torch.uint64, device=dev)
-        kind = torch.empty(n, dtype=torch.uint8, device=dev)
+        handle = _new(n, torch.uint64, dev, stream)
+        kind = _new(n, torch.uint8, dev, stream)
         while True:
-            ws = _workspace(OP_REGISTRY, n, self.capacity, dev, None)
+            ws = _workspace(OP_REGISTRY, n, self.capacity, dev, None, stream)
             rc = lib().dmadesc_reg_register(
                 *self._table(), self.page_shift, _dev(addr, torch.uint64, "addr", n),
                 _dev(size, torch.uint64, "size", n), n, _dev(handle, torch.uint64, "handle", n),
@@ -639,8 +639,8 @@ class DeviceRegistry:
     def deregister(self, handles: torch.Tensor, stream=None) -> torch.Tensor:
         """Returns status u8[n]."""
         n = handles.numel()
-        status = torch.empty(n, dtype=torch.uint8, device=self.device)
-        ws = _workspace(OP_REGISTRY, n, self.capacity, self.device, None)
+        status = _new(n, torch.uint8, self.device, stream)
+        ws = _workspace(OP_REGISTRY, n, self.capacity, self.device, None, stream)
         rc = lib().dmadesc_reg_deregister(
             *self._table(), _dev(handles, torch.uint64, "handle", n), n,
             _dev(status, torch.uint8, "status", n), *ws[1:], _stream(self.device, stream))

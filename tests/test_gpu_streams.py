@@ -8,6 +8,9 @@ import pytest
 import torch
 
 import memory_dma_descriptor_amd as dd
+import oracle
+import synth
+from tests import gpu_cases as gc
 from tests.test_gpu_kv import i32
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +65,38 @@ def test_cache_calls():
     ordered(fresh(lambda s: dd.kv_free(*state, i32([1]), 16, stream=s)))
     ordered(fresh(lambda s: dd.kv_fork(*state, i32([0]), i32([2]), 16, stream=s)))
     ordered(fresh(lambda s: dd.kv_reserve(*state, i32([0, 2]), i32([20, 5]), 16, stream=s)))
+
+
+def test_descriptor_calls():
+    d = synth.generate("tiny", n=500)
+    lut, off, ln, qid = gc.dev(d["lut"]), gc.dev(d["off"]), gc.dev(d["len"]), gc.dev(d["qid"])
+    table = gc.dev(d["rstart"]), gc.dev(d["rend"]), gc.dev(d["rlkey"])
+    bus, nq = d["list_bus_base"], d["nqueues"]
+    pages = oracle.build_prp(d["lut"], d["off"], d["len"], bus, 1 << 50)["total"]
+    pool = torch.zeros((pages, 512), dtype=torch.uint64, device="cuda")
+
+    def same(results):
+        for k, v in results[0].items():
+            assert torch.equal(v, results[1][k]), k
+
+    same(ordered(lambda s: dd.mr_lookup(*table, off, ln, va_base=d["va_base"], stream=s)))
+    same(ordered(lambda s: dd.build_prp(lut, off, ln, bus, pool, stream=s)))
+    same(ordered(lambda s: dd.partition_by_queue(qid, nq, stream=s)))
+    batches = ordered(lambda s: dd.build_batch(lut, off, ln, qid, nq, bus, pool, *table,
+                                               va_base=d["va_base"], stream=s))
+    same(batches)
+    b = batches[0]
+
+    def emit(s):
+        rings = torch.zeros((nq, 8192 * 64), dtype=torch.uint8, device="cuda")
+        depth = gc.dev(np.full(nq, 8192, np.uint32))
+        free = gc.dev(np.full(nq, 8191, np.uint32))
+        tail, cursor = gc.dev(np.zeros(nq, np.uint32)), gc.dev(np.zeros(nq, np.uint64))
+        slba = gc.dev(synth.slba("tiny", d["n"]))
+        addresses = dd.ring_addresses(list(rings))
+        torch.cuda.synchronize()
+        r = dd.emit_sqe(b["perm"], b["qoff"], b["status"], ln, slba, b["prp1"], b["prp2"], addresses,
+                        depth, free, tail, cursor, stream=s)
+        torch.cuda.synchronize()
+        return dict(placed=r["placed"])
+    same(ordered(emit))
