@@ -631,10 +631,14 @@ class DeviceRegistry:
                 _dev(size, torch.uint64, "size", n), n, _dev(handle, torch.uint64, "handle", n),
                 _dev(kind, torch.uint8, "kind", n), self._needed.data_ptr(), *ws[1:], _stream(dev, stream))
             _check("dmadesc_reg_register", rc)
+            if stream is not None:
+                stream.synchronize()                  # the current stream reads the answer
             needed = int(self._needed.view(torch.int64)[0].item())
             if needed <= self.capacity or not grow:
                 return dict(handle=handle, kind=kind, needed=needed)
             self.grow(needed)
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream(dev))    # where the records are copied
 
     def deregister(self, handles: torch.Tensor, stream=None) -> torch.Tensor:
         """Returns status u8[n]."""

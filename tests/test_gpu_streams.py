@@ -100,3 +100,20 @@ def test_descriptor_calls():
         torch.cuda.synchronize()
         return dict(placed=r["placed"])
     same(ordered(emit))
+
+
+def test_registry_calls():
+    addr = gc.dev(np.arange(64, dtype=np.uint64) * np.uint64(1 << 20))
+    size = gc.dev(np.full(64, 4096, np.uint64))
+
+    def register(s):
+        reg = dd.DeviceRegistry()
+        torch.cuda.synchronize()
+        r = reg.register(addr, size, stream=s)           # grows from nothing
+        torch.cuda.synchronize()
+        status = reg.deregister(r["handle"], stream=s)
+        torch.cuda.synchronize()
+        assert (status == dd.DEREG_REMOVED).all() and reg.count() == 0
+        return dict(handle=r["handle"], kind=r["kind"], status=status)
+    a, b = ordered(register)
+    assert all(torch.equal(a[k], b[k]) for k in a)
