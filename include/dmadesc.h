@@ -686,7 +686,8 @@ int dmadesc_kv_check(const dmadesc_kv_cache *cache, const int32_t *q_start, uint
  * for the scale.
  *   k, v       [total][kv_heads][dim] of `type`, with strides in elements
  *              between tokens and heads; dim contiguous. Base 16-byte aligned
- *              and strides multiples of 8 (-EINVAL otherwise)
+ *              and strides multiples of 8, but for that of a single token or head
+ *              (-EINVAL otherwise)
  *   q_start    i32[rows + 1], q_start[0] = 0, non-decreasing, ends at total
  *   total      new tokens of all requests, < 2^31. A call is one launch of 2^24 - 1
  *              workgroups at most: kv_heads * (total / 16 + 2 rows) < 2^25 - 1
@@ -713,7 +714,7 @@ int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_to
  * probability times V scale: terms below 2^-27 of that keep fewer bits, terms
  * below 2^-37 may count as 0 in o (never in lse).
  *   q          [total][heads][dim] of `type` (bf16 or fp16), strides in
- *              elements; base 16-byte aligned, strides multiples of 8
+ *              elements; base and strides as dmadesc_kv_append's
  *   heads      a multiple of kv_heads
  *   scale      factor of the scores; 0 means 1 / sqrt(dim). At most 2.3e38 in size
  *              (-EINVAL). A score past f32's range, and one that is not 0 under a

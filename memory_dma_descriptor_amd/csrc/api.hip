@@ -100,10 +100,12 @@ bool kv_cache_ok(const dmadesc_kv_cache *c)
     return true;
 }
 
-// A [total][heads][dim] operand: 16-byte loads of its rows.
-bool kv_rows_ok(const void *p, int64_t tok, int64_t head)
+// A [total][heads][dim] operand: 16-byte loads of its rows. The stride of a
+// dimension of size 1 is never used.
+bool kv_rows_ok(const void *p, int64_t tok, int64_t head, uint64_t total, uint32_t heads)
 {
-    return p && aligned16(p) && tok >= 0 && head >= 0 && (tok & 7) == 0 && (head & 7) == 0;
+    auto ok = [](int64_t stride, uint64_t n) { return n <= 1 || (stride >= 0 && (stride & 7) == 0); };
+    return p && aligned16(p) && ok(tok, total) && ok(head, heads);
 }
 
 bool kv_pages_ok(const int32_t *refs, uint64_t npages, const int32_t *table, uint32_t rows,
@@ -408,8 +410,8 @@ int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_to
 {
     if (!kv_cache_ok(cache) || total >= (1ull << 31) || type > DMADESC_KV_FP32) return -EINVAL;
     if (total == 0 || cache->rows == 0) return 0;
-    if (!q_start || !kv_rows_ok(k, k_token_stride, k_head_stride) ||
-        !kv_rows_ok(v, v_token_stride, v_head_stride))
+    if (!q_start || !kv_rows_ok(k, k_token_stride, k_head_stride, total, cache->kv_heads) ||
+        !kv_rows_ok(v, v_token_stride, v_head_stride, total, cache->kv_heads))
         return -EINVAL;
     if (dd::kv_append_groups(total, cache->rows, cache->kv_heads) > dd::kKvMaxGroups) return -EINVAL;
     if (cache->npages == 0 || cache->width == 0) return 0;        // no page to write
@@ -438,7 +440,7 @@ int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_to
     if (type > DMADESC_KV_FP16 || heads == 0 || heads % cache->kv_heads) return -EINVAL;
     if (total * heads >= (1ull << 31) || !(fabsf(scale) <= kMaxScale)) return -EINVAL;
     if (total == 0 || cache->rows == 0) return 0;
-    if (!q_start || !kv_rows_ok(q, q_token_stride, q_head_stride)) return -EINVAL;
+    if (!q_start || !kv_rows_ok(q, q_token_stride, q_head_stride, total, heads)) return -EINVAL;
     if (!out || !aligned16(out) || !aligned4(lse)) return -EINVAL;
     const uint64_t tokens = (uint64_t)cache->width * cache->page_tokens;
     if (!dd::kv_attend_fits(total, cache->rows, heads, cache->kv_heads, cache->dim, tokens))

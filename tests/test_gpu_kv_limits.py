@@ -272,3 +272,23 @@ def test_reserve_names_bad_pages():
     assert r["status"].tolist() == [dd.KV_EPAGE, dd.KV_OK, dd.KV_EINVAL, dd.KV_OK, dd.KV_OK, dd.KV_OK]
     assert state[2].tolist() == [3, 17, 1, 17, 3, 17] and state[0].tolist() == [1, 1, 1, 1]
     assert state[1].tolist() == [[9, -1], [-1, 1], [-7, -1], [5, 2], [9, -1], [0, 3]]
+
+
+def test_strides_of_single_tokens_and_heads():
+    # A view of one token, or of one head, may have any stride there.
+    rng = np.random.default_rng(3)
+    pool, table, _ = random_case(rng, [40], [1], 16, 64, kc.E4M3, (-7, -4), 1.0)
+    x = torch.randn((4, 2, 64 + 3), device="cuda").bfloat16()
+    one = x.flatten()[:2 * 64].view(1, 2, 64)
+    odd = one.as_strided((1, 2, 64), (131, 64, 1))
+    head = one.as_strided((2, 1, 64), (64, 5, 1))
+    pools, outs = [], []
+    for k in (one, odd):
+        p = torch.zeros((8, dd.kv_page_bytes(2, 16, 64)), dtype=torch.uint8, device="cuda")
+        dd.kv_append(k, k, i32([0, 1]), p, i32([[0, 3, 5]]), i32([40]), 16)
+        pools.append(p)
+        outs.append(dd.kv_attend(k, i32([0, 1]), p, i32([[0, 3, 5]]), i32([40]), 2, 16)["out"])
+    assert pools[0].any() and torch.equal(*pools) and torch.equal(*outs)
+    outs = [dd.kv_attend(q, i32([0, 2]), torch.from_numpy(pool).cuda(), i32(table), i32([40]), 1, 16)["out"]
+            for q in (one.view(2, 1, 64), head)]
+    assert torch.equal(*outs)

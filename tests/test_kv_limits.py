@@ -75,3 +75,19 @@ def test_attend_sizes_past_a_launch():
         assert (size(total, rows, heads, heads, 64, width, 16) > 0) == (width > 16)
         assert attend(cache(rows=rows, kv_heads=heads, page_tokens=16, width=width), total, heads) \
             not in (0, EINVAL)
+
+
+@no_gpu_only
+def test_strides_of_single_tokens_and_heads_mean_nothing():
+    lib = dd.lib()
+
+    def append(total, heads, tok, head):
+        return lib.dmadesc_kv_append(cache(kv_heads=heads), P, tok, head, P, tok, head, P, total, 0, None)
+
+    for f in (append, lambda total, heads, tok, head: attend(cache(kv_heads=heads), total, heads, 0.0, tok,
+                                                              head)):
+        for tok in (3, -8, 12):
+            assert f(1, 2, tok, 64) not in (0, EINVAL)       # one token: gets as far as a launch
+            assert f(2, 2, tok, 64) == EINVAL
+            assert f(2, 1, 64, tok) not in (0, EINVAL)       # one head
+            assert f(2, 2, 64, tok) == EINVAL
