@@ -764,9 +764,10 @@ def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table:
               causal: bool = True, scale: float | None = None, out: dict | None = None,
               ws: torch.Tensor | None = None, stream=None, check: bool = True) -> dict:
     """Attention of q [total, heads, dim] (bf16 or fp16) over the cache; returns
-    dict(out, lse): out as q, lse f32[total, heads]. scale None means
-    1 / sqrt(dim). check=True first checks the table (kv_check), synchronizes
-    and raises DmadescRefused if a request names a bad page or length."""
+    dict(out, lse): out as q, lse f32[total, heads], which is left out if `out` is
+    given without it. scale None means 1 / sqrt(dim). check=True first checks the
+    table (kv_check), synchronizes and raises DmadescRefused if a request names a
+    bad page or length."""
     if scale is not None:
         in_f32 = ctypes.c_float(scale).value
         if in_f32 == 0:
@@ -791,11 +792,12 @@ def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table:
         need = _kv_attend_bytes(total, rows, heads, kv_heads, dim, width, page_tokens)
         ws = _new(need, torch.uint8, dev, stream) if need else None
     ws_bytes = 0 if ws is None else ws.numel()
+    lse = out.get("lse")
     rc = lib().dmadesc_kv_attend(
         ctypes.byref(cache), *qp, qs, total, heads, _KV_TYPE[q.dtype],
         KV_CAUSAL if causal else 0, 0.0 if scale is None else scale,
         _dev(out["out"], q.dtype, "out", total * heads * dim),
-        _dev(out["lse"], torch.float32, "lse", total * heads),
+        None if lse is None else _dev(lse, torch.float32, "lse", total * heads),
         _dev(ws, torch.uint8, "ws") if ws_bytes else None, ws_bytes, _stream(dev, stream))
     _check("dmadesc_kv_attend", rc)
     return out

@@ -292,3 +292,16 @@ def test_strides_of_single_tokens_and_heads():
     outs = [dd.kv_attend(q, i32([0, 2]), torch.from_numpy(pool).cuda(), i32(table), i32([40]), 1, 16)["out"]
             for q in (one.view(2, 1, 64), head)]
     assert torch.equal(*outs)
+
+
+def test_attend_without_the_log_sum_exp():
+    rng = np.random.default_rng(4)
+    pool, table, q = random_case(rng, [700, 500], [3, 2], 32, 64, kc.E4M3, (-7, -4), 1.0)
+    q = torch.from_numpy(q).bfloat16().cuda()
+    args = (q, i32([0, 3, 5]), torch.from_numpy(pool).cuda(), i32(table), i32([700, 500]), 1, 32)
+    want, out = dd.kv_attend(*args), dict(out=torch.empty_like(q))
+    assert dd.kv_attend(*args, out=out) is out and torch.equal(out["out"], want["out"])
+    many = torch.randn((300, 2, 64), device="cuda").bfloat16()
+    args = (many, i32([0, 100, 300])) + args[2:]
+    want, out = dd.kv_attend(*args), dict(out=torch.empty_like(many), lse=None)
+    assert torch.equal(dd.kv_attend(*args, out=out)["out"], want["out"]) and out["lse"] is None
