@@ -1110,15 +1110,14 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv_join(AttendArgs few, Attend
             all *= exp2_(mine - top);
 #pragma unroll
             for (int d = (int)kLanes / 2; d > 0; d >>= 1) all += __shfl_xor(all, d, kLanes);
-            // Parts count by their share of the row's mass. Shares sum to 1, so that no
-            // sum leaves the range of its parts; they are taken in two factors, since one
-            // alone may lie below f32's range where its part's values are large.
-            const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+            // A part's weight in two factors: alone it may lie below f32's range where its
+            // part's values are large; and over kMaxSplits, so that no sum passes the
+            // range that its parts lie in.
 #pragma unroll 4
             for (uint32_t s = phase; s < plan.y; s += share) {
                 const uint64_t p = (uint64_t)(first + s * step) * tile_rows + in;
                 const float v = exp2_(0.5f * (a.part_lse[p] - top));
-                o += *reinterpret_cast<const f32x4 *>(a.part + p * kD + at * 4) * v * (v * inv);
+                o += *reinterpret_cast<const f32x4 *>(a.part + p * kD + at * 4) * v * (v * (1.0f / kMaxSplits));
             }
         }
         osum[grp][at] = o;
@@ -1127,7 +1126,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv_join(AttendArgs few, Attend
             for (uint32_t k = 1; k < share; ++k) o += osum[grp + k * width][at];
             const uint32_t r = (uint32_t)r0 + row;
             const uint64_t orow = (uint64_t)(s0 + r / a.group) * a.heads + head * a.group + r % a.group;
-            store4<kQ>(a.out, orow * kD + at * 4, o);
+            const float norm = all == 0.0f ? 0.0f : (float)kMaxSplits / all;
+            store4<kQ>(a.out, orow * kD + at * 4, o * norm);
             if (a.lse && at == 0)
                 a.lse[orow] = all == 0.0f ? -kInf : (top + __builtin_log2f(all)) * 0.69314718055994531f;
         }
