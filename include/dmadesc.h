@@ -742,8 +742,9 @@ size_t dmadesc_kv_attend_workspace_bytes(uint64_t total, uint32_t rows, uint32_t
  * Page operations. refs i32[npages] counts the rows that hold each page (0 =
  * free); table and lens are as in dmadesc_kv_cache and are updated in place.
  * A row of n tokens holds the pages of its first ceil(n / page_tokens) table
- * entries. The listed rows of one call are distinct, and no row is both
- * parent and child (otherwise the result is unspecified but memory-safe).
+ * entries. The rows that a call changes (row, child, slot) are each listed once,
+ * and no row is both parent and child (otherwise the result is unspecified but
+ * memory-safe); one parent may have several children.
  * status u8[n] (enum dmadesc_kv_status): a refused row is left as it was. Table
  * entries outside the pool are otherwise passed over: they have no references to
  * drop or to gain.

@@ -8,10 +8,12 @@
 // the matrix cores in the 16-bit type that holds every code exactly, the
 // powers of two are applied to the f32 scores and to the probabilities. What
 // the product with V gets is p_t 2^(e_t) relative to the row's running
-// maximum M of (s_t + e_t), times 2^15, in f16: at most 2^15, with 11 bits
-// down to 2^-29 of the largest term, so many small terms keep their weight
-// and a block with a small scale keeps its precision. That rounding (2^-12 of
-// each term) is the only one below f32 before the output's.
+// maximum M of (s_t + e_t), in f16, where the largest stands at 2^14 (few rows)
+// or 2^13 to 2^15 (many): 11 bits down to 2^-27 of the largest term, fewer to
+// 2^-37, so many small terms keep their weight and a block with a small scale
+// keeps its precision. That rounding (2^-11 of each term at most) is the only
+// one below f32 before the output's. In two bf16 parts, which would keep more,
+// the second product would run twice.
 //
 // Layout. Scores are computed transposed, S^T = K Q^T: the 16x16x32 product
 // puts query rows on the lanes (lane % 16) and four tokens in each lane's
@@ -361,8 +363,8 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 // fourth tile of a piece of the cache, 16 KB (D = 128) each in flight while the
 // tile before is multiplied. Two waves a SIMD keep 128 KB of a compute unit's reads
 // outstanding. 64 requests of 200 to 9,000 tokens, 32 heads on 8, D = 128, e4m3:
-// 123 us for 706 MB, 5.7 TB/s (a large copy: 4.9); 4 of 100,000 to 131,072
-// tokens: 151 us, 6.4 TB/s. One tile alone takes 6 us, most of it the launch and
+// 130 us, 730 MB read and written, 5.6 TB/s (a large copy: 4.9); 4 of 100,000 to
+// 131,072 tokens: 159 us, 6.2 TB/s. One tile alone takes 6 us, most of it the launch and
 // fetching 14 KB of code for the first time; each further one of a wave 1.3 us.
 template <int kD, int kQ, int kCodes, int kNt>
 __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(AttendArgs a)
@@ -699,9 +701,9 @@ __device__ __forceinline__ float half_max(float x)
 // 8 c + 7 are tokens 8 h .. 8 h + 7 of block c (h = lane / 32), which is the
 // order in which the second product takes them.
 //
-// Here the vector unit has as much to do as the matrix unit (a tile of a wave:
-// 1,024 cycles of products, about 210 vector instructions, 32 of them
-// exponentials), so that three things are done differently. The softmax takes one
+// Here the vector unit has more to do than the matrix unit (D = 128, a tile of a
+// wave: 1,024 cycles of products, some 260 vector instructions of 4 cycles, 32 of
+// them exponentials of 16), so that three things are done differently. The softmax takes one
 // reference per row, the running maximum M of s + e: 2^(s + e - M + 13) is both the
 // f16 probability and, times 2^-e once per block, the term of the sum; it moves
 // only when a row passes it by 2^2, so that the accumulators are seldom rescaled
@@ -712,8 +714,9 @@ __device__ __forceinline__ float half_max(float x)
 // its own.) The next codes are converted between the first product's
 // instructions and a block's exponentials taken between the second's. And a wave
 // in a product goes before the other wave of its SIMD. 2,048 tokens over 16,384,
-// 32 heads on 8, D = 128, e4m3: 547 us, 943 TFLOP/s (a library product of 8192^3:
-// 1,217); matrix and vector units are each busy half of the time.
+// 32 heads on 8, D = 128, e4m3: 540 to 555 us by the box, 930 to 950 TFLOP/s (a
+// library product of 8192^3: 1,217). By counters of that launch the matrix unit is busy 45 % of the cycles, the
+// vector unit 63 %, LDS 42 %.
 template <int kD, int kQ, int kCodes>
 __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_kv_attend_many(AttendArgs a)
 {
@@ -1052,7 +1055,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
 // some of the splits. The chunks of 16 are numbered without a scan: request b's
 // first is q_start[b] * group / 16 + b.
 constexpr uint32_t kJoinRows = 16;
-// Threads of its workgroups: 512 where they all run at once (420 of them: 5.0 us,
+// Threads of its workgroups: 512 where they all run at once (420 of them: 5.3 us,
 // with 256 threads 6.2), 256 where they are many and most find nothing to join
 // (4,000: 5.3 us, with 512 threads 9.6).
 constexpr uint32_t kJoinWide = 512, kJoinNarrow = 256, kJoinOnce = 1024;
@@ -1137,11 +1140,15 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv_join(AttendArgs few, Attend
 
 // How a call's memory and launches follow from what the host knows, which is
 // not the requests' own sizes. Up to 32 query rows per key head on the average
-// the kernel of few rows takes all requests, past that the kernel of many rows
-// (35 rows, 33 requests: 43 us by three row tiles of the first, 38 by the second;
-// 28 rows: 32 and 34; D = 256, 32 rows: 27 and 41). Only where some request may
-// have more than 1,024 rows beside those few, a chunk of a prompt among single
-// tokens, are both launched and share the requests: an idle launch costs 4 us.
+// of all table rows the kernel of few rows takes all requests, past that the
+// kernel of many rows (35 rows, 33 requests: 43 us by three row tiles of the
+// first, 38 by the second; 28 rows: 32 and 34; D = 256, 32 rows: 27 and 41). Both
+// are launched and share the requests where that average is at most 32 and one
+// request could have more than 1,024 rows if each other table row brought a
+// token: an idle launch costs 4 us. The average is no rule for uneven batches:
+// 63 requests of a token (123 us alone) and a chunk of 2,048 over 4,096 (134) take
+// 281 us together, the chunk of 512 tokens of one request 24 us alone and 49 in a
+// table of 512 rows that bring nothing.
 struct Launch {
     uint32_t tile_rows;          // of the kernel of few rows: one product's 16, or 32
     uint32_t few, many;          // workgroups (= partial results) of each kernel

@@ -10,8 +10,8 @@
 // which every later block adds up for itself: the counts of a million pages
 // are 512 words, cheaper to read again than another launch or a look-back.
 // Bound: the launches and the dependent loads for a few rows (free, fork, reserve
-// and copy for 24 rows: 2.7, 2.7, 3.1 + 5.0 and 2.6 us; for 4,096 rows and 410,000
-// pages 3.7, 4.7, 4.0 + 8.8 and 6.6 us), HBM bytes of the copied pages where there
+// and copy for 24 rows: 2.7, 2.8, 3.3 + 5.3 and 2.8 us; for 4,096 rows and 410,000
+// pages 3.6, 4.7, 4.2 + 9.2 and 6.2 us), HBM bytes of the copied pages where there
 // are many.
 #include "dd_internal.h"
 #include "dd_kv.hpp"
