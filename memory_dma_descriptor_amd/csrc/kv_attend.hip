@@ -714,7 +714,7 @@ __device__ __forceinline__ float half_max(float x)
 // its own.) The next codes are converted between the first product's
 // instructions and a block's exponentials taken between the second's. And a wave
 // in a product goes before the other wave of its SIMD. 2,048 tokens over 16,384,
-// 32 heads on 8, D = 128, e4m3: 540 to 555 us by the box, 930 to 950 TFLOP/s (a
+// 32 heads on 8, D = 128, e4m3: 540 to 555 us by the card, 930 to 950 TFLOP/s (a
 // library product of 8192^3: 1,217). By counters of that launch the matrix unit is busy 45 % of the cycles, the
 // vector unit 63 %, LDS 42 %.
 template <int kD, int kQ, int kCodes>
