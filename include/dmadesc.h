@@ -43,7 +43,15 @@
  *   dmadesc_kv_free / _fork / _reserve / _copy_pages / _compact
  *                              end, branch and extend requests, copy shared
  *                              pages, gather the live pages at the front
- *   dmadesc_kv_check           which requests name bad pages or lengths
+ *   dmadesc_kv_read            keys and values back in 16 or 32 bits
+ *   dmadesc_kv_check / _tree_check / _read_check
+ *                              which requests name bad pages or lengths
+ *
+ * and a decoding step with trees of drafted tokens over that cache:
+ *
+ *   dmadesc_kv_attend_tree     attention of a tree of new tokens, each along its path
+ *   dmadesc_verify_drafts      which of them the target accepts, and the next token
+ *   dmadesc_kv_keep            the accepted ones together in the cache
  *
  * Sources (web pages, cited by title and section):
  *   [NCCL-26] "NCCL 专家课程 26：GPUDirect RDMA、DMA-BUF、MR 与注册缓存",
@@ -737,6 +745,121 @@ int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_to
 size_t dmadesc_kv_attend_workspace_bytes(uint64_t total, uint32_t rows, uint32_t heads,
                                          uint32_t kv_heads, uint32_t dim, uint32_t width,
                                          uint32_t page_tokens);
+
+/*
+ * Trees of drafted tokens. Request r's new tokens are rows q_start[r] ..
+ * q_start[r+1]-1, at most DMADESC_TREE_MOST of them; parent i32[total] holds for
+ * each the row, within its request, of the token before it: less than its own, or
+ * -1 for none. A step is dmadesc_kv_reserve, dmadesc_kv_append (of all of them),
+ * dmadesc_kv_attend_tree, dmadesc_verify_drafts, dmadesc_kv_keep and dmadesc_kv_free.
+ *
+ * dmadesc_kv_attend_tree: dmadesc_kv_attend for trees. Token j of a request with n
+ * new tokens sees the t < lens[r] - n cached before them, itself and the tokens on
+ * its way up the tree; one at a place before the cache's first (a request with
+ * more new tokens than length) is not there. Arguments, results, limits and
+ * workspace as dmadesc_kv_attend's, with
+ *   parent     i32[total]. A parent that is no earlier token of the request counts as
+ *              -1; tokens past the DMADESC_TREE_MOST-th of a request give unspecified
+ *              results (memory-safe; dmadesc_kv_tree_check refuses both)
+ *
+ * dmadesc_kv_tree_check: as dmadesc_kv_check with `appending`, and EINVAL for
+ * requests of more than DMADESC_TREE_MOST new tokens or with bad parents.
+ */
+#define DMADESC_TREE_MOST 512
+int dmadesc_kv_attend_tree(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride,
+                           int64_t q_head_stride, const int32_t *q_start, const int32_t *parent,
+                           uint64_t total, uint32_t heads, uint32_t type, float scale, void *out,
+                           float *lse, void *ws, size_t ws_bytes, void *stream);
+int dmadesc_kv_tree_check(const dmadesc_kv_cache *cache, const int32_t *q_start, const int32_t *parent,
+                          uint64_t total, uint8_t *status, void *stream);
+
+/*
+ * dmadesc_verify_drafts - verification of drafted tokens against the target's
+ * probabilities, from given random numbers.
+ *
+ * A request's row 0 is its last sure token, the others are drafts below it. From
+ * row 0 on, at node v with target row p = probs[v] and draft row d = draft[v],
+ * v's children (rows j with parent[j] = v, in order) are tried, token x = tokens[j]:
+ *   with draft, the children having been drawn from d one after another, none
+ *   twice; c = 0, W = 1, Q = 1 at first:
+ *     accepted if u[j] d(x) W < max(p(x) - c d(x), 0) Q
+ *     refused otherwise: c += W / Q, W = sum_t max(p(t) - c d(t), 0), Q -= d(x); where
+ *     that W is 0, c and W stay. A child with d(x) = 0, or with Q <= 0, is passed over
+ *   without (draft NULL: the drafts are certain); M = 1 at first:
+ *     accepted if u[j] M < p(x), refused otherwise: M -= p(x) and x has no part any
+ *     more. A child with p(x) = 0 is passed over
+ *   A token outside [0, vocab) and one refused at v before are passed over.
+ * An accepted child is the next v. Where no child is accepted, the next token is
+ * the least t with w(t) > 0 and sum_{s <= t} w(s) > u[row 0] sum_s w(s), w(t) being
+ * max(p(t) - c d(t), 0), or p(t) without the refused tokens; where such a w has no
+ * mass, w as it was before the last refusal. If the sums never pass (u of 1 or more,
+ * or NaN) it is the last t with w(t) > 0, and -1 if there is none. This makes
+ * the accepted tokens and the next one a sample of the target. Probabilities
+ * that are not positive and finite count as 0; tests and sums are f64.
+ *   probs, draft  [total][vocab] of `type` (enum dmadesc_kv_type), rows `stride`
+ *              elements apart; draft may be NULL. Row j: after the token of row j.
+ *              Rows without children are not read from draft unless v ends there
+ *   tokens     i32[total] token of each row (row 0's is not looked at)
+ *   parent     i32[total]; row 0's is not looked at
+ *   u          f32[total] in [0, 1): of row j > 0 for its test, of row 0 for the draw
+ *   vocab      1 .. 2^31 - 1; rows < 2^22 and rows * ceil(vocab / 4096) < 2^24 (-EINVAL)
+ *   path       i32[total]: accepted rows of each request in order, row 0 first, within
+ *              the request, from q_start[r] on; -1 behind them
+ *   count      i32[rows]: how many they are (0: the request has no rows)
+ *   next       i32[rows]: the next token (-1: the request has no rows)
+ *   status     u8[rows] enum dmadesc_kv_status: EINVAL for q_start out of order, more
+ *              than DMADESC_TREE_MOST rows or a bad parent (count 0, next -1)
+ * Workspace: dmadesc_verify_drafts_workspace_bytes(total, rows, vocab).
+ */
+int dmadesc_verify_drafts(const void *probs, int64_t probs_stride, const void *draft, int64_t draft_stride,
+                          uint64_t vocab, uint32_t type, const int32_t *tokens, const int32_t *parent,
+                          const int32_t *q_start, uint32_t rows, uint64_t total, const float *u,
+                          int32_t *path, int32_t *count, int32_t *next, uint8_t *status, void *ws,
+                          size_t ws_bytes, void *stream);
+size_t dmadesc_verify_drafts_workspace_bytes(uint64_t total, uint32_t rows, uint64_t vocab);
+
+/*
+ * dmadesc_kv_keep - brings the accepted tokens of each request together.
+ *
+ * Of the n new tokens of request r (the last of its lens[r], base = lens[r] - n),
+ * token base + path[q_start[r] + k] goes to place base + k for k < count[r]; path
+ * ascends. Where no token moves, nothing is written. From the first that moves on,
+ * the blocks are written as dmadesc_kv_append would write these tokens' cached
+ * values (code times scale) there: the least scale that holds them, but no smaller
+ * one than that of earlier tokens in the block, codes rounded once, the earlier
+ * tokens' again where the scale grew. Places behind the last kept token keep their
+ * codes. The pages written are held by this request alone, as append's are.
+ *   path, count  as dmadesc_verify_drafts gives them
+ *   keep       i32[rows]: base + count[r], what dmadesc_kv_free cuts the row to;
+ *              lens[r] where the request is refused. Not lens itself (-EINVAL)
+ *   status     u8[rows] enum dmadesc_kv_status: EINVAL for a bad length, q_start out of
+ *              order, more than DMADESC_TREE_MOST new tokens or more than length, a count
+ *              past them or a path that does not ascend in 0 .. n - 1; EPAGE for a new
+ *              token on a page outside the pool. A refused request is left as it was
+ * rows * kv_heads < 2^25 - 1 (-EINVAL).
+ */
+int dmadesc_kv_keep(const dmadesc_kv_cache *cache, const int32_t *path, const int32_t *count,
+                    const int32_t *q_start, uint64_t total, int32_t *keep, uint8_t *status, void *stream);
+
+/*
+ * dmadesc_kv_read - keys and values of cached tokens in 16 or 32 bits.
+ *
+ * Tokens first[r] .. of request r, start[r+1] - start[r] of them, go to rows start[r] ..
+ * of k and v: code times scale, rounded once to `type` (to infinity past its range).
+ * Tokens past the length, before 0 or on a page outside the pool read as 0.
+ *   first      i32[rows] or NULL: 0 for all
+ *   start      i32[rows + 1], start[0] = 0, non-decreasing, ends at total
+ *   k, v       [total][kv_heads][dim] of `type`, written; strides as
+ *              dmadesc_kv_append's, and no two elements at one place
+ *   total      < 2^31, kv_heads * (total / 16 + 2 rows) < 2^25 - 1 (-EINVAL otherwise)
+ * dmadesc_kv_read_check: status u8[rows], EINVAL for `start` out of order or tokens past
+ * the length or before 0, EPAGE for tokens on pages outside the pool.
+ */
+int dmadesc_kv_read(const dmadesc_kv_cache *cache, const int32_t *first, const int32_t *start,
+                    uint64_t total, uint32_t type, void *k, int64_t k_token_stride, int64_t k_head_stride,
+                    void *v, int64_t v_token_stride, int64_t v_head_stride, void *stream);
+int dmadesc_kv_read_check(const dmadesc_kv_cache *cache, const int32_t *first, const int32_t *start,
+                          uint64_t total, uint8_t *status, void *stream);
 
 /*
  * Page operations. refs i32[npages] counts the rows that hold each page (0 =

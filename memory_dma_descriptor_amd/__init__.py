@@ -26,7 +26,8 @@ __all__ = ["mr_lookup", "build_prp", "build_prp_packed", "build_prp_packed_noall
            "MISS", "EXACT", "CONTAINED", "INVALID",
            "PRP_OK", "PRP_EINVAL", "PRP_ERANGE", "PRP_ENOSPC", "PRP_EBUSY",
            "kv_page_bytes", "kv_append", "kv_attend", "kv_check", "kv_free", "kv_fork",
-           "kv_reserve", "kv_compact", "kv_copy_pages",
+           "kv_reserve", "kv_compact", "kv_copy_pages", "kv_attend_tree", "kv_tree_check",
+           "verify_drafts", "kv_keep", "kv_read", "kv_read_check", "TREE_MOST",
            "KV_E4M3", "KV_INT8", "KV_OK", "KV_EINVAL", "KV_EPAGE", "KV_ENOSPC"]
 
 LIB_PATH = _build.LIB
@@ -37,6 +38,7 @@ OP_KV_RESERVE, OP_KV_COMPACT = 7, 8
 KV_E4M3, KV_INT8 = 0, 1
 KV_OK, KV_EINVAL, KV_EPAGE, KV_ENOSPC = 0, 1, 2, 3
 KV_CAUSAL = 1
+TREE_MOST = 512                  # new tokens of a request's tree
 _KV_MAX_SCALE = 2.3e38           # times log2(e) still a float32
 REG_MAX_BATCH, REG_MAX_CAPACITY = 65536, 1 << 24
 REG_INVALID, REG_HIT, REG_NEW, REG_HIT_NEW, REG_NOSPACE = 0, 1, 2, 3, 4
@@ -89,6 +91,15 @@ _EXPORTS = {
     "dmadesc_kv_attend": ([_P, _P, _I64, _I64, _P, _U64, _U32, _U32, _U32, ctypes.c_float,
                            _P, _P, _P, _SIZE, _P], ctypes.c_int),
     "dmadesc_kv_attend_workspace_bytes": ([_U64, _U32, _U32, _U32, _U32, _U32, _U32], _SIZE),
+    "dmadesc_kv_attend_tree": ([_P, _P, _I64, _I64, _P, _P, _U64, _U32, _U32, ctypes.c_float,
+                                _P, _P, _P, _SIZE, _P], ctypes.c_int),
+    "dmadesc_kv_tree_check": ([_P, _P, _P, _U64, _P, _P], ctypes.c_int),
+    "dmadesc_verify_drafts": ([_P, _I64, _P, _I64, _U64, _U32, _P, _P, _P, _U32, _U64, _P, _P, _P,
+                               _P, _P, _P, _SIZE, _P], ctypes.c_int),
+    "dmadesc_verify_drafts_workspace_bytes": ([_U64, _U32, _U64], _SIZE),
+    "dmadesc_kv_keep": ([_P, _P, _P, _P, _U64, _P, _P, _P], ctypes.c_int),
+    "dmadesc_kv_read": ([_P, _P, _P, _U64, _U32, _P, _I64, _I64, _P, _I64, _I64, _P], ctypes.c_int),
+    "dmadesc_kv_read_check": ([_P, _P, _P, _U64, _P, _P], ctypes.c_int),
     "dmadesc_kv_free": ([_P, _U64, _P, _P, _U32, _U32, _U32, _P, _P, _U64, _P, _P], ctypes.c_int),
     "dmadesc_kv_fork": ([_P, _U64, _P, _P, _U32, _U32, _U32, _P, _P, _U64, _P, _P], ctypes.c_int),
     "dmadesc_kv_reserve": ([_P, _U64, _P, _P, _U32, _U32, _U32, _P, _P, _U64, _P, _P, _P, _P,
@@ -759,15 +770,9 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, pool: tor
     _check("dmadesc_kv_append", rc)
 
 
-def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table: torch.Tensor,
-              lens: torch.Tensor, kv_heads: int, page_tokens: int, codes: int = KV_E4M3,
-              causal: bool = True, scale: float | None = None, out: dict | None = None,
-              ws: torch.Tensor | None = None, stream=None, check: bool = True) -> dict:
-    """Attention of q [total, heads, dim] (bf16 or fp16) over the cache; returns
-    dict(out, lse): out as q, lse f32[total, heads], which is left out if `out` is
-    given without it. scale None means 1 / sqrt(dim). check=True first checks the
-    table (kv_check), synchronizes and raises DmadescRefused if a request names a
-    bad page or length."""
+def _attend(func, q, q_start, tree, pool, table, lens, kv_heads, page_tokens, codes, causal, scale, out,
+            ws, stream, check):
+    """kv_attend, or with `tree` (parent,) kv_attend_tree."""
     if scale is not None:
         in_f32 = ctypes.c_float(scale).value
         if in_f32 == 0:
@@ -780,10 +785,14 @@ def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table:
     cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes)
     qp = _kv_rows(q, "q", total, heads, dim, (torch.bfloat16, torch.float16))
     qs = _dev(q_start, torch.int32, "q_start", cache.rows + 1)
+    up = tuple(_dev(p, torch.int32, "parent", total) for p in tree)
     if check:
-        status = kv_check(q_start, total, pool, table, lens, kv_heads, page_tokens, dim, False,
-                          stream)
-        _kv_refused("dmadesc_kv_attend", status, stream, dict(status=status))
+        if tree:
+            status = kv_tree_check(q_start, tree[0], pool, table, lens, kv_heads, page_tokens, dim, stream)
+        else:
+            status = kv_check(q_start, total, pool, table, lens, kv_heads, page_tokens, dim, False,
+                              stream)
+        _kv_refused(func, status, stream, dict(status=status))
     if out is None:
         out = dict(out=_new((total, heads, dim), q.dtype, dev, stream),
                    lse=_new((total, heads), torch.float32, dev, stream))
@@ -793,13 +802,181 @@ def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table:
         ws = _new(need, torch.uint8, dev, stream) if need else None
     ws_bytes = 0 if ws is None else ws.numel()
     lse = out.get("lse")
-    rc = lib().dmadesc_kv_attend(
-        ctypes.byref(cache), *qp, qs, total, heads, _KV_TYPE[q.dtype],
-        KV_CAUSAL if causal else 0, 0.0 if scale is None else scale,
-        _dev(out["out"], q.dtype, "out", total * heads * dim),
+    flags = () if tree else (KV_CAUSAL if causal else 0,)
+    rc = getattr(lib(), func)(
+        ctypes.byref(cache), *qp, qs, *up, total, heads, _KV_TYPE[q.dtype], *flags,
+        0.0 if scale is None else scale, _dev(out["out"], q.dtype, "out", total * heads * dim),
         None if lse is None else _dev(lse, torch.float32, "lse", total * heads),
         _dev(ws, torch.uint8, "ws") if ws_bytes else None, ws_bytes, _stream(dev, stream))
-    _check("dmadesc_kv_attend", rc)
+    _check(func, rc)
+    return out
+
+
+def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table: torch.Tensor,
+              lens: torch.Tensor, kv_heads: int, page_tokens: int, codes: int = KV_E4M3,
+              causal: bool = True, scale: float | None = None, out: dict | None = None,
+              ws: torch.Tensor | None = None, stream=None, check: bool = True) -> dict:
+    """Attention of q [total, heads, dim] (bf16 or fp16) over the cache; returns
+    dict(out, lse): out as q, lse f32[total, heads], which is left out if `out` is
+    given without it. scale None means 1 / sqrt(dim). check=True first checks the
+    table (kv_check), synchronizes and raises DmadescRefused if a request names a
+    bad page or length."""
+    return _attend("dmadesc_kv_attend", q, q_start, (), pool, table, lens, kv_heads, page_tokens, codes,
+                   causal, scale, out, ws, stream, check)
+
+
+def kv_attend_tree(q: torch.Tensor, q_start: torch.Tensor, parent: torch.Tensor, pool: torch.Tensor,
+                   table: torch.Tensor, lens: torch.Tensor, kv_heads: int, page_tokens: int,
+                   codes: int = KV_E4M3, scale: float | None = None, out: dict | None = None,
+                   ws: torch.Tensor | None = None, stream=None, check: bool = True) -> dict:
+    """kv_attend for trees of new tokens: token j of a request sees what was cached
+    before the request's new tokens, itself and the tokens on its way up the tree,
+    parent i32[total] (rows within the request, each less than its own, -1: none).
+    check=True first checks the table and the trees (kv_tree_check), synchronizes
+    and raises DmadescRefused."""
+    return _attend("dmadesc_kv_attend_tree", q, q_start, (parent,), pool, table, lens, kv_heads,
+                   page_tokens, codes, True, scale, out, ws, stream, check)
+
+
+def kv_tree_check(q_start: torch.Tensor, parent: torch.Tensor, pool: torch.Tensor, table: torch.Tensor,
+                  lens: torch.Tensor, kv_heads: int, page_tokens: int, dim: int,
+                  stream=None) -> torch.Tensor:
+    """Status u8[rows] of a cache and the trees of its new tokens: KV_OK, KV_EINVAL
+    (also for more than TREE_MOST of them, or a parent that is no earlier one),
+    KV_EPAGE."""
+    cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, 0)
+    status = _new(table.shape[0], torch.uint8, pool.device, stream)
+    rc = lib().dmadesc_kv_tree_check(ctypes.byref(cache),
+                                     _dev(q_start, torch.int32, "q_start", table.shape[0] + 1),
+                                     _dev(parent, torch.int32, "parent"), parent.numel(),
+                                     status.data_ptr(), _stream(pool.device, stream))
+    _check("dmadesc_kv_tree_check", rc)
+    return status
+
+
+def _rows_of(t, name, total, vocab, dtype):
+    """(pointer, row stride) of a [total, vocab] operand."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor, got {t.device}")
+    if t.dtype != dtype or dtype not in _KV_TYPE:
+        raise TypeError(f"{name}: {t.dtype} is not taken")
+    if t.shape != (total, vocab):
+        raise ValueError(f"{name}: expected shape {(total, vocab)}, got {tuple(t.shape)}")
+    if t.stride(1) != 1 and vocab > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), t.stride(0)
+
+
+@functools.lru_cache(maxsize=4096)
+def _verify_bytes(total, rows, vocab):
+    return int(lib().dmadesc_verify_drafts_workspace_bytes(total, rows, vocab))
+
+
+def verify_drafts(probs: torch.Tensor, tokens: torch.Tensor, parent: torch.Tensor, q_start: torch.Tensor,
+                  u: torch.Tensor, draft: torch.Tensor | None = None, out: dict | None = None,
+                  ws: torch.Tensor | None = None, stream=None, check: bool = True) -> dict:
+    """Which drafted tokens the target accepts, and the token after them.
+
+    Request r's rows are q_start[r] .. q_start[r+1]-1, the first its last sure token,
+    the others a tree of drafts below it (`tokens`, `parent` i32[total]). probs and
+    draft [total, vocab] (f32, bf16 or fp16) hold the target's and the draft's
+    probabilities after each row's token; siblings were drawn from the draft's row
+    one after another, none twice. draft None: the drafts are certain. u f32[total] in
+    [0, 1): a row's for its test, the first row's for the next token.
+
+    Returns dict(path i32[total], count, next i32[rows], status u8[rows]): the accepted
+    rows of each request in order, the first row among them, -1 behind them; how many
+    they are; the next token. check=True synchronizes and raises DmadescRefused for
+    refused requests (q_start out of order, a bad parent, more than TREE_MOST rows)."""
+    if probs.dim() != 2:
+        raise ValueError("probs must be [total, vocab]")
+    total, vocab = probs.shape
+    rows = q_start.numel() - 1
+    dev = probs.device
+    if rows < 0:
+        raise ValueError("q_start must be i32[rows + 1]")
+    p = _rows_of(probs, "probs", total, vocab, probs.dtype)
+    d = (None, 0) if draft is None else _rows_of(draft, "draft", total, vocab, probs.dtype)
+    if out is None:
+        out = dict(path=_new(total, torch.int32, dev, stream), count=_new(rows, torch.int32, dev, stream),
+                   next=_new(rows, torch.int32, dev, stream), status=_new(rows, torch.uint8, dev, stream))
+    if ws is None:
+        ws = _new(max(_verify_bytes(total, rows, vocab), 1), torch.uint8, dev, stream)
+    rc = lib().dmadesc_verify_drafts(
+        *p, *d, vocab, _KV_TYPE[probs.dtype], _dev(tokens, torch.int32, "tokens", total),
+        _dev(parent, torch.int32, "parent", total), _dev(q_start, torch.int32, "q_start"), rows, total,
+        _dev(u, torch.float32, "u", total), _dev(out["path"], torch.int32, "path", total),
+        _dev(out["count"], torch.int32, "count", rows), _dev(out["next"], torch.int32, "next", rows),
+        _dev(out["status"], torch.uint8, "status", rows), _dev(ws, torch.uint8, "ws"), ws.numel(),
+        _stream(dev, stream))
+    _check("dmadesc_verify_drafts", rc)
+    if check:
+        _kv_refused("dmadesc_verify_drafts", out["status"], stream, out)
+    return out
+
+
+def kv_keep(path: torch.Tensor, count: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor,
+            table: torch.Tensor, lens: torch.Tensor, kv_heads: int, page_tokens: int, dim: int,
+            codes: int = KV_E4M3, stream=None, check: bool = True) -> dict:
+    """Moves the accepted new tokens of each request (`path` and `count` of
+    verify_drafts) together, to the places right behind those cached before them;
+    returns dict(keep i32[rows], status u8[rows]): the tokens that kv_free(keep=...)
+    then cuts the rows to. check=True synchronizes and raises DmadescRefused for
+    refused requests, which are left as they were."""
+    cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes)
+    rows, total = table.shape[0], path.numel()
+    out = dict(keep=_new(rows, torch.int32, pool.device, stream),
+               status=_new(rows, torch.uint8, pool.device, stream))
+    rc = lib().dmadesc_kv_keep(
+        ctypes.byref(cache), _dev(path, torch.int32, "path"), _dev(count, torch.int32, "count", rows),
+        _dev(q_start, torch.int32, "q_start", rows + 1), total, out["keep"].data_ptr(),
+        out["status"].data_ptr(), _stream(pool.device, stream))
+    _check("dmadesc_kv_keep", rc)
+    if check:
+        _kv_refused("dmadesc_kv_keep", out["status"], stream, out)
+    return out
+
+
+def kv_read_check(first: torch.Tensor | None, start: torch.Tensor, total: int, pool: torch.Tensor,
+                  table: torch.Tensor, lens: torch.Tensor, kv_heads: int, page_tokens: int, dim: int,
+                  stream=None) -> torch.Tensor:
+    """Status u8[rows] of what kv_read is to read: KV_OK, KV_EINVAL, KV_EPAGE."""
+    cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, 0)
+    rows = table.shape[0]
+    status = _new(rows, torch.uint8, pool.device, stream)
+    rc = lib().dmadesc_kv_read_check(
+        ctypes.byref(cache), None if first is None else _dev(first, torch.int32, "first", rows),
+        _dev(start, torch.int32, "start", rows + 1), total, status.data_ptr(), _stream(pool.device, stream))
+    _check("dmadesc_kv_read_check", rc)
+    return status
+
+
+def kv_read(first: torch.Tensor | None, start: torch.Tensor, total: int, pool: torch.Tensor,
+            table: torch.Tensor, lens: torch.Tensor, kv_heads: int, page_tokens: int, dim: int,
+            codes: int = KV_E4M3, dtype: torch.dtype = torch.bfloat16, out: dict | None = None,
+            stream=None, check: bool = True) -> dict:
+    """Keys and values of cached tokens in bf16, fp16 or f32: tokens first[r] .. of
+    request r (None: from 0 on) go to rows start[r] .. start[r+1]-1 of k and v, which
+    dict(k, v) holds, [total, kv_heads, dim]. `out` gives them (strided views
+    included; their type counts). check=True first checks what is asked for
+    (kv_read_check), synchronizes and raises DmadescRefused."""
+    cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes)
+    rows, dev = table.shape[0], pool.device
+    if out is None:
+        if dtype not in _KV_TYPE:
+            raise TypeError(f"dtype: {dtype} is not taken")
+        out = {x: _new((total, kv_heads, dim), dtype, dev, stream) for x in "kv"}
+    dtype = out["k"].dtype
+    kp = _kv_rows(out["k"], "k", total, kv_heads, dim, _KV_TYPE)
+    vp = _kv_rows(out["v"], "v", total, kv_heads, dim, (dtype,))
+    f = None if first is None else _dev(first, torch.int32, "first", rows)
+    s = _dev(start, torch.int32, "start", rows + 1)
+    if check:
+        status = kv_read_check(first, start, total, pool, table, lens, kv_heads, page_tokens, dim, stream)
+        _kv_refused("dmadesc_kv_read", status, stream, dict(status=status))
+    rc = lib().dmadesc_kv_read(ctypes.byref(cache), f, s, total, _KV_TYPE[dtype], *kp, *vp,
+                               _stream(dev, stream))
+    _check("dmadesc_kv_read", rc)
     return out
 
 

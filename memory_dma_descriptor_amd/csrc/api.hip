@@ -108,6 +108,13 @@ bool kv_rows_ok(const void *p, int64_t tok, int64_t head, uint64_t total, uint32
     return p && aligned16(p) && ok(tok, total) && ok(head, heads);
 }
 
+// A launch of 1,024 threads a request, and one of 256 for every part of a row.
+bool verify_sizes_ok(uint32_t rows, uint64_t vocab)
+{
+    return rows > 0 && rows < (1u << 22) && vocab > 0 && vocab < (1ull << 31) &&
+           dd::verify_groups(rows, vocab) <= dd::kKvMaxGroups;
+}
+
 bool kv_pages_ok(const int32_t *refs, uint64_t npages, const int32_t *table, uint32_t rows,
                  uint32_t width, uint32_t page_tokens)
 {
@@ -431,10 +438,13 @@ size_t dmadesc_kv_attend_workspace_bytes(uint64_t total, uint32_t rows, uint32_t
     return dd::ws_kv_attend(total, rows, heads, kv_heads, dim, (uint64_t)width * page_tokens);
 }
 
-int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride,
-                      int64_t q_head_stride, const int32_t *q_start, uint64_t total,
-                      uint32_t heads, uint32_t type, uint32_t flags, float scale, void *out,
-                      float *lse, void *ws, size_t ws_bytes, void *stream)
+namespace {
+
+// dmadesc_kv_attend, or with `tree` dmadesc_kv_attend_tree.
+int attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+           const int32_t *q_start, bool tree, const int32_t *parent, uint64_t total, uint32_t heads,
+           uint32_t type, uint32_t flags, float scale, void *out, float *lse, void *ws, size_t ws_bytes,
+           void *stream)
 {
     if (!kv_cache_ok(cache) || total >= (1ull << 31) || (flags & ~DMADESC_KV_CAUSAL)) return -EINVAL;
     if (type > DMADESC_KV_FP16 || heads == 0 || heads % cache->kv_heads) return -EINVAL;
@@ -442,6 +452,7 @@ int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_to
     if (total == 0 || cache->rows == 0) return 0;
     if (!q_start || !kv_rows_ok(q, q_token_stride, q_head_stride, total, heads)) return -EINVAL;
     if (!out || !aligned16(out) || !aligned4(lse)) return -EINVAL;
+    if (tree && (!parent || !aligned4(parent))) return -EINVAL;
     const uint64_t tokens = (uint64_t)cache->width * cache->page_tokens;
     if (!dd::kv_attend_fits(total, cache->rows, heads, cache->kv_heads, cache->dim, tokens))
         return -EINVAL;
@@ -449,8 +460,109 @@ int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_to
                                          tokens);
     if (need > 0 && !ws_ok(ws, ws_bytes, need)) return -EINVAL;
     dd::KvAttendArgs a{*cache, q, q_token_stride, q_head_stride, q_start, total, heads, type,
-                       (flags & DMADESC_KV_CAUSAL) != 0, scale, out, lse, ws};
+                       (flags & DMADESC_KV_CAUSAL) != 0, scale, out, lse, ws, parent};
     return launched(dd::launch_kv_attend(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride,
+                      int64_t q_head_stride, const int32_t *q_start, uint64_t total,
+                      uint32_t heads, uint32_t type, uint32_t flags, float scale, void *out,
+                      float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    return attend(cache, q, q_token_stride, q_head_stride, q_start, false, nullptr, total, heads, type,
+                  flags, scale, out, lse, ws, ws_bytes, stream);
+}
+
+int dmadesc_kv_attend_tree(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride,
+                           int64_t q_head_stride, const int32_t *q_start, const int32_t *parent,
+                           uint64_t total, uint32_t heads, uint32_t type, float scale, void *out,
+                           float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    return attend(cache, q, q_token_stride, q_head_stride, q_start, true, parent, total, heads, type,
+                  DMADESC_KV_CAUSAL, scale, out, lse, ws, ws_bytes, stream);
+}
+
+int dmadesc_kv_tree_check(const dmadesc_kv_cache *cache, const int32_t *q_start, const int32_t *parent,
+                          uint64_t total, uint8_t *status, void *stream)
+{
+    if (!kv_cache_ok(cache) || total >= (1ull << 31)) return -EINVAL;
+    if (cache->rows == 0) return 0;
+    if (!q_start || !aligned4(q_start) || (total > 0 && (!parent || !aligned4(parent))) || !status)
+        return -EINVAL;
+    return launched(dd::launch_kv_tree_check(*cache, q_start, parent, total, status,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int dmadesc_kv_keep(const dmadesc_kv_cache *cache, const int32_t *path, const int32_t *count,
+                    const int32_t *q_start, uint64_t total, int32_t *keep, uint8_t *status, void *stream)
+{
+    if (!kv_cache_ok(cache) || total >= (1ull << 31)) return -EINVAL;
+    if (cache->rows == 0) return 0;
+    if ((total > 0 && (!path || !aligned4(path))) || !count || !aligned4(count) || !q_start ||
+        !aligned4(q_start) || !keep || !aligned4(keep) || keep == cache->lens || !status)
+        return -EINVAL;
+    if (dd::kv_keep_groups(cache->rows, cache->kv_heads) > dd::kKvMaxGroups) return -EINVAL;
+    dd::KvKeepArgs a{*cache, path, count, q_start, total, keep, status};
+    return launched(dd::launch_kv_keep(a, static_cast<hipStream_t>(stream)));
+}
+
+int dmadesc_kv_read_check(const dmadesc_kv_cache *cache, const int32_t *first, const int32_t *start,
+                          uint64_t total, uint8_t *status, void *stream)
+{
+    if (!kv_cache_ok(cache) || total >= (1ull << 31)) return -EINVAL;
+    if (cache->rows == 0) return 0;
+    if (!aligned4(first) || !start || !aligned4(start) || !status) return -EINVAL;
+    return launched(dd::launch_kv_read_check(*cache, first, start, total, status,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int dmadesc_kv_read(const dmadesc_kv_cache *cache, const int32_t *first, const int32_t *start,
+                    uint64_t total, uint32_t type, void *k, int64_t k_token_stride, int64_t k_head_stride,
+                    void *v, int64_t v_token_stride, int64_t v_head_stride, void *stream)
+{
+    if (!kv_cache_ok(cache) || total >= (1ull << 31) || type > DMADESC_KV_FP32) return -EINVAL;
+    if (total == 0 || cache->rows == 0) return 0;
+    if (!aligned4(first) || !start || !aligned4(start) ||
+        !kv_rows_ok(k, k_token_stride, k_head_stride, total, cache->kv_heads) ||
+        !kv_rows_ok(v, v_token_stride, v_head_stride, total, cache->kv_heads))
+        return -EINVAL;
+    if (dd::kv_read_groups(total, cache->rows, cache->kv_heads) > dd::kKvMaxGroups) return -EINVAL;
+    dd::KvReadArgs a{*cache, first, start, total, type, k, v, k_token_stride, k_head_stride,
+                     v_token_stride, v_head_stride};
+    return launched(dd::launch_kv_read(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t dmadesc_verify_drafts_workspace_bytes(uint64_t total, uint32_t rows, uint64_t vocab)
+{
+    if (total >= (1ull << 31) || !verify_sizes_ok(rows, vocab)) return 0;
+    return dd::ws_verify(total, rows, vocab);
+}
+
+int dmadesc_verify_drafts(const void *probs, int64_t probs_stride, const void *draft, int64_t draft_stride,
+                          uint64_t vocab, uint32_t type, const int32_t *tokens, const int32_t *parent,
+                          const int32_t *q_start, uint32_t rows, uint64_t total, const float *u,
+                          int32_t *path, int32_t *count, int32_t *next, uint8_t *status, void *ws,
+                          size_t ws_bytes, void *stream)
+{
+    if (total >= (1ull << 31) || type > DMADESC_KV_FP32) return -EINVAL;
+    if (rows == 0) return 0;
+    if (!verify_sizes_ok(rows, vocab)) return -EINVAL;
+    if (!q_start || !aligned4(q_start) || !count || !aligned4(count) || !next || !aligned4(next) || !status)
+        return -EINVAL;
+    const uintptr_t in_row = type == DMADESC_KV_FP32 ? 3u : 1u;
+    auto row_ok = [&](const void *p, int64_t stride) {
+        return (reinterpret_cast<uintptr_t>(p) & in_row) == 0 && (total <= 1 || stride >= 0);
+    };
+    if (total > 0 && (!probs || !row_ok(probs, probs_stride) || !row_ok(draft, draft_stride) || !tokens ||
+                      !aligned4(tokens) || !parent || !aligned4(parent) || !u || !aligned4(u) || !path ||
+                      !aligned4(path)))
+        return -EINVAL;
+    if (!ws_ok(ws, ws_bytes, dd::ws_verify(total, rows, vocab))) return -EINVAL;
+    dd::VerifyArgs a{probs, draft, probs_stride, draft_stride, type, vocab, tokens, parent, q_start, rows,
+                     total, u, path, count, next, status, ws};
+    return launched(dd::launch_verify(a, static_cast<hipStream_t>(stream)));
 }
 
 int dmadesc_kv_free(int32_t *refs, uint64_t npages, int32_t *table, int32_t *lens, uint32_t rows,

@@ -118,6 +118,39 @@ struct KvAttendArgs {
     void *out;
     float *lse;                             // or nullptr
     void *ws;
+    const int32_t *parent = nullptr;        // of a tree of new tokens
+};
+
+struct KvReadArgs {
+    dmadesc_kv_cache cache;
+    const int32_t *first;                   // or nullptr: 0
+    const int32_t *start;
+    uint64_t total;
+    uint32_t type;
+    void *k, *v;
+    int64_t k_tok, k_head, v_tok, v_head;   // strides in elements
+};
+
+struct KvKeepArgs {
+    dmadesc_kv_cache cache;
+    const int32_t *path, *count, *q_start;
+    uint64_t total;
+    int32_t *keep;
+    uint8_t *status;
+};
+
+struct VerifyArgs {
+    const void *probs, *draft;              // draft: or nullptr
+    int64_t probs_row, draft_row;           // strides in elements
+    uint32_t type;
+    uint64_t vocab;
+    const int32_t *tokens, *parent, *q_start;
+    uint32_t rows;
+    uint64_t total;
+    const float *u;
+    int32_t *path, *count, *next;
+    uint8_t *status;
+    void *ws;
 };
 
 struct KvPageArgs {
@@ -169,6 +202,17 @@ hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s);
 hipError_t launch_kv_attend(const KvAttendArgs &a, hipStream_t s);
 hipError_t launch_kv_check(const dmadesc_kv_cache &c, const int32_t *q_start, uint64_t total,
                            bool appending, uint8_t *status, hipStream_t s);
+hipError_t launch_kv_tree_check(const dmadesc_kv_cache &c, const int32_t *q_start,
+                                const int32_t *parent, uint64_t total, uint8_t *status, hipStream_t s);
+uint64_t kv_read_groups(uint64_t total, uint32_t rows, uint32_t kv_heads);
+hipError_t launch_kv_read(const KvReadArgs &a, hipStream_t s);
+hipError_t launch_kv_read_check(const dmadesc_kv_cache &c, const int32_t *first, const int32_t *start,
+                                uint64_t total, uint8_t *status, hipStream_t s);
+uint64_t kv_keep_groups(uint32_t rows, uint32_t kv_heads);
+hipError_t launch_kv_keep(const KvKeepArgs &a, hipStream_t s);
+hipError_t launch_verify(const VerifyArgs &a, hipStream_t s);
+uint64_t verify_groups(uint32_t rows, uint64_t vocab);
+size_t ws_verify(uint64_t total, uint32_t rows, uint64_t vocab);
 hipError_t launch_kv_free(const KvPageArgs &k, const int32_t *row, const int32_t *keep,
                           hipStream_t s);
 hipError_t launch_kv_fork(const KvPageArgs &k, const int32_t *parent, const int32_t *child,

@@ -1,5 +1,5 @@
 // kv_attend.hip - attention of new tokens over a paged 8-bit key/value cache,
-// for gfx950.
+// a chunk's in order or a tree's along its paths, for gfx950.
 //
 // Mathematics. For a query row q and the cached tokens t it sees,
 //   s_t = scale q.K_t,  o = sum_t 2^(s_t log2 e - m) V_t / l,  l = sum_t 2^(..)
@@ -56,6 +56,7 @@ struct AttendArgs {
     const void *q;
     int64_t q_tok, q_head;
     const int32_t *q_start;
+    const int32_t *parent;                  // [total] of a tree of new tokens (kTree)
     uint32_t total, heads, group;
     int causal;
     float scale;                            // times log2 e
@@ -353,6 +354,68 @@ __device__ __forceinline__ void note_nan(int *first_nan, uint32_t nans, int dim,
     if (nans) atomicMin(&first_nan[dim], tok + (__builtin_ctz(nans) >> 3));
 }
 
+// Trees of new tokens. Row j sees the cache before the tree and the nodes of its
+// own path, which a bit each of `seen` says. Only the tiles that hold nodes need
+// them: the rest of the cache is seen by all rows. Two words of zeros follow, so
+// that places past the last node read as not seen; the stride is odd.
+constexpr int kTreeMost = (int)DMADESC_TREE_MOST;
+constexpr int kTreeWords = kTreeMost / 32 + 2, kTreeStride = kTreeWords + 1;
+
+template <int kRows>
+struct TreeRows {
+    uint32_t seen[kRows][kTreeStride];
+    int16_t up[kTreeMost];
+    uint32_t nans;                          // a NaN code of V was taken out of a tile with nodes
+
+    // The paths of query rows row0 .. row0 + kRows - 1 of the request whose
+    // tokens start at s0. A parent that is no earlier node ends the path, so every
+    // walk ends. Called by the whole workgroup; has barriers.
+    __device__ __forceinline__ void fill(const AttendArgs &a, uint32_t s0, uint32_t news, uint32_t row0)
+    {
+        const uint32_t r = row0 + threadIdx.x, last = (row0 + kRows - 1) / a.group + 1;
+        uint32_t nodes = news < last ? news : last;
+        nodes = nodes < (uint32_t)kTreeMost ? nodes : (uint32_t)kTreeMost;
+        for (uint32_t i = threadIdx.x; i < nodes; i += kThreads) {
+            const int32_t p = a.parent[s0 + i];
+            up[i] = (int16_t)(p >= 0 && (uint32_t)p < i ? p : -1);
+        }
+        for (int i = (int)threadIdx.x; i < kRows * kTreeStride; i += kThreads) (&seen[0][0])[i] = 0;
+        __syncthreads();
+        if (threadIdx.x < (uint32_t)kRows && r / a.group < nodes)
+            for (int k = (int)(r / a.group); k >= 0; k = up[k]) atomicOr(&seen[threadIdx.x][k >> 5], 1u << (k & 31));
+        __syncthreads();
+    }
+
+    // Which of the tokens i0 .. i0 + 31 the row sees, counted from the first node on;
+    // tokens before it are seen.
+    __device__ __forceinline__ uint32_t bits(int row, int i0) const
+    {
+        const int i = i0 < 0 ? 0 : i0, w = i >> 5 < kTreeWords - 2 ? i >> 5 : kTreeWords - 2;
+        const uint64_t two = (uint64_t)seen[row][w + 1] << 32 | seen[row][w];
+        const uint32_t v = (uint32_t)(two >> (i & 31));
+        return i0 >= 0 ? v : i0 <= -32 ? ~0u : v << -i0 | ((1u << -i0) - 1u);
+    }
+};
+
+// Whether V has a NaN in dimension `dim` of a token in from .. to - 1 that the row
+// sees. For the rows of a tree, whose tokens no limit describes, this is looked up
+// in the pages at the end, if a tile had a NaN at all.
+template <int kD, int kRows>
+__device__ bool tree_nan(const TreeRows<kRows> &tree, const KvView &c, const int32_t *tab, uint32_t head,
+                         int row, int base, int from, int to, int dim)
+{
+    const int per = (int)c.tshift - 4;
+    for (int t = from; t < to; ++t) {
+        if (!(tree.bits(row, t - base) & 1u)) continue;
+        const uint32_t page = (uint32_t)tab[t >> c.tshift], sub = (uint32_t)(t / kBlock) & ((1u << per) - 1u);
+        if (page >= c.npages) continue;
+        const uint8_t code = c.pool[(uint64_t)page * c.page_bytes + c.code_bytes +
+                                    (uint64_t)((head << per) + sub) * (kBlock * kD) + dim * kBlock + t % kBlock];
+        if ((code & 0x7f) == 0x7f) return true;
+    }
+    return false;
+}
+
 constexpr float kInf = __builtin_inff();
 
 // 2^x for -inf..; x finite or -inf.
@@ -366,7 +429,7 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 // 130 us, 730 MB read and written, 5.6 TB/s (a large copy: 4.9); 4 of 100,000 to
 // 131,072 tokens: 159 us, 6.2 TB/s. One tile alone takes 6 us, most of it the launch and
 // fetching 14 KB of code for the first time; each further one of a wave 1.3 us.
-template <int kD, int kQ, int kCodes, int kNt>
+template <int kD, int kQ, int kCodes, int kNt, bool kTree>
 __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(AttendArgs a)
 {
     constexpr int kRows = 16 * kNt;
@@ -375,11 +438,16 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
     typedef typename QFrag<kQ>::type Q8;
     __shared__ f32x4 obuf[kWaves][kNt * kX][kWave];
     __shared__ float stat[3][kWaves][kRows];
-    __shared__ int first_nan[kD];
+    __shared__ int first_nan[kTree ? 1 : kD];
+    __shared__ TreeRows<kTree ? kRows : 1> tree;
 
     Item it;
     if (!Plan<kRows, kThreads, slots_few(kD, kNt), 4, kWholeFew, kLongFew>::find(a, blockIdx.x, it)) return;
-    for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
+    if constexpr (kTree) {
+        if (threadIdx.x == 0) tree.nans = 0;
+    } else {
+        for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
+    }
     __syncthreads();
     const KvView &c = a.c;
     const int ln = lane(), col = ln & 15, g = ln >> 4;
@@ -398,9 +466,9 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
     Q8 qf[kNt][kC][2];
     int limit[kNt];
     int low = len - 1, high = len - 1;      // least and largest limit of the tile's rows
-    if (a.causal) {
+    if (kTree || a.causal) {
         const uint32_t last = nrows - 1 < row0 + kRows - 1 ? nrows - 1 : row0 + kRows - 1;
-        low = len - news + (int)(row0 / a.group);
+        low = len - news + (kTree ? -1 : (int)(row0 / a.group));
         high = len - news + (int)(last / a.group);
     }
 #pragma unroll
@@ -408,7 +476,7 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
         const uint32_t r = row0 + n * 16 + col;
         const bool on = r < nrows;
         const uint32_t rr = on ? r : 0u, j = rr / a.group, h = head * a.group + rr % a.group;
-        limit[n] = !on ? -1 : a.causal ? len - news + (int)j : len - 1;
+        limit[n] = !on ? -1 : kTree || a.causal ? len - news + (int)j : len - 1;
         const uint16_t *const q = static_cast<const uint16_t *>(a.q) +
                                   (int64_t)(s0 + j) * a.q_tok + (int64_t)h * a.q_head + 16 * g;
 #pragma unroll
@@ -435,6 +503,7 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
     const int t1 = t0 + part < see ? t0 + part : see;
     const int last_block = len > 0 ? (len - 1) / kBlock : 0;
     const int32_t *const tab = c.table + (uint64_t)b * c.width;
+    if (kTree && t1 * kTile - 1 > low) tree.fill(a, s0, (uint32_t)news, row0);
     const int kblk = col >> 2;              // block of the lane's key rows
     int32_t pk = 0, pv = 0;                 // pages of the next tile, per lane
     u32x4 kr[4][kC], vr[kX];
@@ -531,13 +600,19 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
 #pragma unroll
             for (int n = 0; n < kNt; ++n) {
                 const int lim = nvalid == 0 ? -1 : limit[n];
+                uint32_t sees = 0;                        // of a tree: the block's tokens, a bit each
+                if (kTree && lim >= 0) {
+                    sees = ~0u;
+                    if (edge) sees = tree.bits(n * 16 + col, tok - (len - news));
+                }
                 float top = -kInf;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float v = s[n][j][i] * kscale;
-                        s[n][j][i] = tok + 4 * j + i <= lim ? v : -kInf;
+                        const bool see_it = kTree ? sees >> (4 * j + i) & 1u : tok + 4 * j + i <= lim;
+                        s[n][j][i] = see_it ? v : -kInf;
                         top = fmaxf(top, s[n][j][i]);
                     }
                 float topv = top == -kInf ? -kInf : top + ve;
@@ -586,7 +661,8 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const uint32_t z = nan_bytes(vr[x][q]);
-                            note_nan(first_nan, z, 16 * x + col, tok + 4 * q);
+                            if constexpr (kTree) tree.nans = 1;       // every writer writes 1
+                            else note_nan(first_nan, z, 16 * x + col, tok + 4 * q);
                             vr[x][q] = without(vr[x][q], z);
                         }
                 }
@@ -657,7 +733,15 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
 #pragma unroll
             for (int w = 1; w < kWaves; ++w) o += obuf[w][n * kX + x][ln];
             o *= norm;
-            if (kCodes == DMADESC_KV_E4M3) {
+            if constexpr (kCodes == DMADESC_KV_E4M3 && kTree) {
+                if (tree.nans) {
+                    const int edge0 = len - news > t0 * kTile ? (len - news) / kTile * kTile : t0 * kTile;
+                    for (int i = 0; i < 4; ++i)
+                        if (tree_nan<kD>(tree, c, tab, head, n * 16 + col, len - news, edge0,
+                                         t1 * kTile < len ? t1 * kTile : len, 16 * x + 4 * g + i))
+                            o[i] = __builtin_nanf("");
+                }
+            } else if constexpr (kCodes == DMADESC_KV_E4M3) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (first_nan[16 * x + 4 * g + i] <= lim) o[i] = __builtin_nanf("");
@@ -717,7 +801,7 @@ __device__ __forceinline__ float half_max(float x)
 // 32 heads on 8, D = 128, e4m3: 540 to 555 us by the card, 930 to 950 TFLOP/s (a
 // library product of 8192^3: 1,217). By counters of that launch the matrix unit is busy 45 % of the cycles, the
 // vector unit 63 %, LDS 42 %.
-template <int kD, int kQ, int kCodes>
+template <int kD, int kQ, int kCodes, bool kTree>
 __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_kv_attend_many(AttendArgs a)
 {
     constexpr int kK = kD / 16;                     // steps of the first product
@@ -735,11 +819,16 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     __shared__ __align__(16) uint8_t kbuf[2][kD / 8 * kChunkStride];
     __shared__ __align__(16) uint8_t vbuf[2][kTile * kD * 2];
     __shared__ float scales[2][3][4];   // [buffer][scale of K, exponent of V, 2^(kSum - kLift - that)][block]
-    __shared__ int first_nan[kD];
+    __shared__ int first_nan[kTree ? 1 : kD];
+    __shared__ TreeRows<kTree ? kRows : 1> tree;
 
     Item it;
     if (!Plan<kRows, kThreads, slots_many(kD), 4, kWholeMany, kLongMany>::find(a, blockIdx.x, it)) return;
-    for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
+    if constexpr (kTree) {
+        if (threadIdx.x == 0) tree.nans = 0;
+    } else {
+        for (int d = (int)threadIdx.x; d < kD; d += kThreads) first_nan[d] = kNoNan;
+    }
     __syncthreads();
     const KvView &c = a.c;
     const int ln = lane(), col = ln & 31, h = ln >> 5, tid = (int)threadIdx.x;
@@ -756,11 +845,11 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
 
     // Least and largest limit of the workgroup's rows, least of the wave's.
     int low = len - 1, high = len - 1, wlow = len - 1;
-    if (a.causal) {
+    if (kTree || a.causal) {
         const uint32_t last = nrows - 1 < row0 + kRows - 1 ? nrows - 1 : row0 + kRows - 1;
-        low = len - news + (int)(row0 / a.group);
+        low = len - news + (kTree ? -1 : (int)(row0 / a.group));
         high = len - news + (int)(last / a.group);
-        wlow = len - news + (int)(wrow0 / a.group);
+        wlow = len - news + (kTree ? -1 : (int)(wrow0 / a.group));
     }
     const int see = high < 0 ? 0 : high / kTile + 1;
     const int part = (see + (int)it.splits - 1) / (int)it.splits;
@@ -771,7 +860,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     const uint32_t r = wrow0 + col;
     const bool on = r < nrows;
     const uint32_t jq = on ? r / a.group : 0u, hq = head * a.group + (on ? r % a.group : 0u);
-    const int limit = !on ? -1 : a.causal ? len - news + (int)jq : len - 1;
+    const int limit = !on ? -1 : kTree || a.causal ? len - news + (int)jq : len - 1;
     {
         const uint16_t *const q = static_cast<const uint16_t *>(a.q) +
                                   (int64_t)(s0 + jq) * a.q_tok + (int64_t)hq * a.q_head + 8 * h;
@@ -796,6 +885,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     // the next 64 are loaded 16 tiles ahead. Tiles past the last are staged too
     // (from addresses inside a page) and not used.
     const int32_t *const tab = c.table + (uint64_t)b * c.width;
+    if (kTree && t1 * kTile - 1 > low) tree.fill(a, s0, (uint32_t)news, row0);
     const int last_block = len > 0 ? (len - 1) / kBlock : 0;
     u32x4 kr[kLoads], vr[kLoads];
     float sc = 0.0f;
@@ -840,7 +930,8 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
                 for (int q = 0; q < 4; ++q) {
                     vr[i][q] &= keep_mask(len - tok0, q);
                     const uint32_t z = nan_bytes(vr[i][q]);
-                    note_nan(first_nan, z, in, tok0 + 4 * q);
+                    if constexpr (!kTree) note_nan(first_nan, z, in, tok0 + 4 * q);
+                    else if (z) tree.nans = 1;                        // every writer writes 1
                     vr[i][q] = without(vr[i][q], z);
                 }
             }
@@ -953,12 +1044,18 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
             wide |= fabsf(ve[i]) > 40.0f;
         }
         if (t * kTile + kTile - 1 > wlow) {
+            uint32_t sees[4];                           // of a tree: the blocks' tokens, a bit each
+            if constexpr (kTree)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sees[i] = on ? tree.bits(wv * 32 + col, t * kTile + i * 16 + 8 * h - (len - news)) : 0u;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int tok = t * kTile + u * 32 + (i >> 3) * 16 + 8 * h + (i & 7);
-                    s[u][i] = tok <= limit ? s[u][i] : -kInf;
+                    if constexpr (!kTree) s[u][i] = tok <= limit ? s[u][i] : -kInf;
+                    else s[u][i] = sees[u * 2 + (i >> 3)] >> (i & 7) & 1u ? s[u][i] : -kInf;
                 }
         }
         // The reference moves where a row's maximum has risen far enough.
@@ -1036,7 +1133,20 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
             f32x4 o = f32x4{acc[x][4 * i], acc[x][4 * i + 1], acc[x][4 * i + 2],
                             acc[x][4 * i + 3]} * norm;
             const int d = 32 * x + 8 * i + 4 * h;
-            if (kCodes == DMADESC_KV_E4M3) {
+            if constexpr (kCodes == DMADESC_KV_E4M3 && kTree) {
+                if (tree.nans) {
+                    const int edge0 = len - news > t0 * kTile ? (len - news) / kTile * kTile : t0 * kTile;
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const bool nan = tree_nan<kD>(tree, c, tab, head, wv * 32 + col, len - news, edge0,
+                                                      t1 * kTile < len ? t1 * kTile : len, d + k);
+                        o[0] = nan && k == 0 ? __builtin_nanf("") : o[0];
+                        o[1] = nan && k == 1 ? __builtin_nanf("") : o[1];
+                        o[2] = nan && k == 2 ? __builtin_nanf("") : o[2];
+                        o[3] = nan && k == 3 ? __builtin_nanf("") : o[3];
+                    }
+                }
+            } else if constexpr (kCodes == DMADESC_KV_E4M3) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     if (first_nan[d + k] <= limit) o[k] = __builtin_nanf("");
@@ -1202,14 +1312,21 @@ Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_head
     return p;
 }
 
+template <int kD, int kQ, int kCodes, bool kTree>
+void launch_kind(const AttendArgs &few, const AttendArgs &many, const Launch &p, hipStream_t s)
+{
+    if (p.many) k_kv_attend_many<kD, kQ, kCodes, kTree><<<p.many, kThreads, 0, s>>>(many);
+    if (p.few) {
+        if (p.tile_rows == 16) k_kv_attend<kD, kQ, kCodes, 1, kTree><<<p.few, kThreads, 0, s>>>(few);
+        else k_kv_attend<kD, kQ, kCodes, 2, kTree><<<p.few, kThreads, 0, s>>>(few);
+    }
+}
+
 template <int kD, int kQ, int kCodes>
 void launch_all(const AttendArgs &few, const AttendArgs &many, const Launch &p, hipStream_t s)
 {
-    if (p.many) k_kv_attend_many<kD, kQ, kCodes><<<p.many, kThreads, 0, s>>>(many);
-    if (p.few) {
-        if (p.tile_rows == 16) k_kv_attend<kD, kQ, kCodes, 1><<<p.few, kThreads, 0, s>>>(few);
-        else k_kv_attend<kD, kQ, kCodes, 2><<<p.few, kThreads, 0, s>>>(few);
-    }
+    if (few.parent) launch_kind<kD, kQ, kCodes, true>(few, many, p, s);
+    else launch_kind<kD, kQ, kCodes, false>(few, many, p, s);
     if (p.join && p.join <= kJoinOnce)
         k_kv_join<kD, kQ, kJoinWide><<<p.join, kJoinWide, 0, s>>>(few, many, p.tile_rows);
     else if (p.join)
@@ -1257,6 +1374,7 @@ hipError_t launch_kv_attend(const KvAttendArgs &k, hipStream_t s)
     few.q_tok = k.q_tok;
     few.q_head = k.q_head;
     few.q_start = k.q_start;
+    few.parent = k.parent;
     few.total = (uint32_t)k.total;
     few.heads = k.heads;
     few.group = k.heads / c.kv_heads;

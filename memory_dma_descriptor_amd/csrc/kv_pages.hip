@@ -75,6 +75,34 @@ __global__ __launch_bounds__(kThreads) void k_kv_check(KvView c, const int32_t *
         status[b] = inval ? DMADESC_KV_EINVAL : bad ? DMADESC_KV_EPAGE : DMADESC_KV_OK;
 }
 
+// As k_kv_check for a call that brings trees: also refuses requests of more new
+// tokens than a tree may have, and parents that are no earlier token of theirs.
+__global__ __launch_bounds__(kThreads) void k_kv_tree_check(KvView c, const int32_t *q_start,
+                                                           const int32_t *parent, uint32_t total,
+                                                           uint8_t *status)
+{
+    __shared__ uint32_t bad, wrong;
+    const uint32_t b = blockIdx.x;
+    if (threadIdx.x == 0) bad = wrong = 0;
+    __syncthreads();
+    const int64_t len = c.lens[b], s0 = q_start[b], s1 = q_start[b + 1], n = s1 - s0;
+    const bool inval = len < 0 || len > ((int64_t)c.width << c.tshift) || s0 < 0 || n < 0 || s1 > total ||
+                       (b == 0 && s0 != 0) || (b == c.rows - 1 && s1 != total) || n > len ||
+                       n > (int64_t)DMADESC_TREE_MOST;
+    if (!inval) {
+        for (int64_t i = threadIdx.x; i < n; i += kThreads) {
+            const int32_t p = parent[s0 + i];
+            if (p < -1 || p >= i) wrong = 1;                    // every writer writes 1
+        }
+        const uint32_t pages = (uint32_t)((len + (1 << c.tshift) - 1) >> c.tshift);
+        for (uint32_t k = threadIdx.x; k < pages; k += kThreads)
+            if ((uint32_t)c.table[(uint64_t)b * c.width + k] >= c.npages) bad = 1;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        status[b] = inval || wrong ? DMADESC_KV_EINVAL : bad ? DMADESC_KV_EPAGE : DMADESC_KV_OK;
+}
+
 // One block per listed row: drops the references of the columns past `keep`
 // tokens and clears them.
 __global__ __launch_bounds__(kThreads) void k_kv_free(Table t, const int32_t *row,
@@ -484,6 +512,13 @@ hipError_t launch_kv_check(const dmadesc_kv_cache &c, const int32_t *q_start, ui
                            bool appending, uint8_t *status, hipStream_t s)
 {
     k_kv_check<<<c.rows, kThreads, 0, s>>>(kv_view(c), q_start, (uint32_t)total, appending, status);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_tree_check(const dmadesc_kv_cache &c, const int32_t *q_start,
+                                const int32_t *parent, uint64_t total, uint8_t *status, hipStream_t s)
+{
+    k_kv_tree_check<<<c.rows, kThreads, 0, s>>>(kv_view(c), q_start, parent, (uint32_t)total, status);
     return hipGetLastError();
 }
 
