@@ -794,29 +794,26 @@ int dmadesc_kv_tree_check(const dmadesc_kv_cache *cache, const int32_t *q_start,
  * max(p(t) - c d(t), 0), or p(t) without the refused tokens; where such a w has no
  * mass, w as it was before the last refusal. If the sums never pass (u of 1 or more,
  * or NaN) it is the last t with w(t) > 0, and -1 if there is none. This makes
- * the accepted tokens and the next one a sample of the target. Probabilities
- * that are not positive and finite count as 0; tests and sums are f64.
+ * the accepted tokens and the next one a sample of the target. Probabilities that
+ * are negative or NaN count as 0, infinity as f32's largest; tests and sums are f64.
  *   probs, draft  [total][vocab] of `type` (enum dmadesc_kv_type), rows `stride`
  *              elements apart; draft may be NULL. Row j: after the token of row j.
  *              Rows without children are not read from draft unless v ends there
  *   tokens     i32[total] token of each row (row 0's is not looked at)
  *   parent     i32[total]; row 0's is not looked at
  *   u          f32[total] in [0, 1): of row j > 0 for its test, of row 0 for the draw
- *   vocab      1 .. 2^31 - 1; rows < 2^22 and rows * ceil(vocab / 4096) < 2^24 (-EINVAL)
+ *   vocab      1 .. 2^31 - 1; rows < 2^22 (-EINVAL)
  *   path       i32[total]: accepted rows of each request in order, row 0 first, within
  *              the request, from q_start[r] on; -1 behind them
  *   count      i32[rows]: how many they are (0: the request has no rows)
  *   next       i32[rows]: the next token (-1: the request has no rows)
  *   status     u8[rows] enum dmadesc_kv_status: EINVAL for q_start out of order, more
  *              than DMADESC_TREE_MOST rows or a bad parent (count 0, next -1)
- * Workspace: dmadesc_verify_drafts_workspace_bytes(total, rows, vocab).
  */
 int dmadesc_verify_drafts(const void *probs, int64_t probs_stride, const void *draft, int64_t draft_stride,
                           uint64_t vocab, uint32_t type, const int32_t *tokens, const int32_t *parent,
                           const int32_t *q_start, uint32_t rows, uint64_t total, const float *u,
-                          int32_t *path, int32_t *count, int32_t *next, uint8_t *status, void *ws,
-                          size_t ws_bytes, void *stream);
-size_t dmadesc_verify_drafts_workspace_bytes(uint64_t total, uint32_t rows, uint64_t vocab);
+                          int32_t *path, int32_t *count, int32_t *next, uint8_t *status, void *stream);
 
 /*
  * dmadesc_kv_keep - brings the accepted tokens of each request together.

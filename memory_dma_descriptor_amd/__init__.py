@@ -95,8 +95,7 @@ _EXPORTS = {
                                 _P, _P, _P, _SIZE, _P], ctypes.c_int),
     "dmadesc_kv_tree_check": ([_P, _P, _P, _U64, _P, _P], ctypes.c_int),
     "dmadesc_verify_drafts": ([_P, _I64, _P, _I64, _U64, _U32, _P, _P, _P, _U32, _U64, _P, _P, _P,
-                               _P, _P, _P, _SIZE, _P], ctypes.c_int),
-    "dmadesc_verify_drafts_workspace_bytes": ([_U64, _U32, _U64], _SIZE),
+                               _P, _P, _P], ctypes.c_int),
     "dmadesc_kv_keep": ([_P, _P, _P, _P, _U64, _P, _P, _P], ctypes.c_int),
     "dmadesc_kv_read": ([_P, _P, _P, _U64, _U32, _P, _I64, _I64, _P, _I64, _I64, _P], ctypes.c_int),
     "dmadesc_kv_read_check": ([_P, _P, _P, _U64, _P, _P], ctypes.c_int),
@@ -867,14 +866,9 @@ def _rows_of(t, name, total, vocab, dtype):
     return t.data_ptr(), t.stride(0)
 
 
-@functools.lru_cache(maxsize=4096)
-def _verify_bytes(total, rows, vocab):
-    return int(lib().dmadesc_verify_drafts_workspace_bytes(total, rows, vocab))
-
-
 def verify_drafts(probs: torch.Tensor, tokens: torch.Tensor, parent: torch.Tensor, q_start: torch.Tensor,
                   u: torch.Tensor, draft: torch.Tensor | None = None, out: dict | None = None,
-                  ws: torch.Tensor | None = None, stream=None, check: bool = True) -> dict:
+                  stream=None, check: bool = True) -> dict:
     """Which drafted tokens the target accepts, and the token after them.
 
     Request r's rows are q_start[r] .. q_start[r+1]-1, the first its last sure token,
@@ -900,15 +894,12 @@ def verify_drafts(probs: torch.Tensor, tokens: torch.Tensor, parent: torch.Tenso
     if out is None:
         out = dict(path=_new(total, torch.int32, dev, stream), count=_new(rows, torch.int32, dev, stream),
                    next=_new(rows, torch.int32, dev, stream), status=_new(rows, torch.uint8, dev, stream))
-    if ws is None:
-        ws = _new(max(_verify_bytes(total, rows, vocab), 1), torch.uint8, dev, stream)
     rc = lib().dmadesc_verify_drafts(
         *p, *d, vocab, _KV_TYPE[probs.dtype], _dev(tokens, torch.int32, "tokens", total),
         _dev(parent, torch.int32, "parent", total), _dev(q_start, torch.int32, "q_start"), rows, total,
         _dev(u, torch.float32, "u", total), _dev(out["path"], torch.int32, "path", total),
         _dev(out["count"], torch.int32, "count", rows), _dev(out["next"], torch.int32, "next", rows),
-        _dev(out["status"], torch.uint8, "status", rows), _dev(ws, torch.uint8, "ws"), ws.numel(),
-        _stream(dev, stream))
+        _dev(out["status"], torch.uint8, "status", rows), _stream(dev, stream))
     _check("dmadesc_verify_drafts", rc)
     if check:
         _kv_refused("dmadesc_verify_drafts", out["status"], stream, out)

@@ -108,13 +108,6 @@ bool kv_rows_ok(const void *p, int64_t tok, int64_t head, uint64_t total, uint32
     return p && aligned16(p) && ok(tok, total) && ok(head, heads);
 }
 
-// A launch of 1,024 threads a request, and one of 256 for every part of a row.
-bool verify_sizes_ok(uint32_t rows, uint64_t vocab)
-{
-    return rows > 0 && rows < (1u << 22) && vocab > 0 && vocab < (1ull << 31) &&
-           dd::verify_groups(rows, vocab) <= dd::kKvMaxGroups;
-}
-
 bool kv_pages_ok(const int32_t *refs, uint64_t npages, const int32_t *table, uint32_t rows,
                  uint32_t width, uint32_t page_tokens)
 {
@@ -534,21 +527,14 @@ int dmadesc_kv_read(const dmadesc_kv_cache *cache, const int32_t *first, const i
     return launched(dd::launch_kv_read(a, static_cast<hipStream_t>(stream)));
 }
 
-size_t dmadesc_verify_drafts_workspace_bytes(uint64_t total, uint32_t rows, uint64_t vocab)
-{
-    if (total >= (1ull << 31) || !verify_sizes_ok(rows, vocab)) return 0;
-    return dd::ws_verify(total, rows, vocab);
-}
-
 int dmadesc_verify_drafts(const void *probs, int64_t probs_stride, const void *draft, int64_t draft_stride,
                           uint64_t vocab, uint32_t type, const int32_t *tokens, const int32_t *parent,
                           const int32_t *q_start, uint32_t rows, uint64_t total, const float *u,
-                          int32_t *path, int32_t *count, int32_t *next, uint8_t *status, void *ws,
-                          size_t ws_bytes, void *stream)
+                          int32_t *path, int32_t *count, int32_t *next, uint8_t *status, void *stream)
 {
     if (total >= (1ull << 31) || type > DMADESC_KV_FP32) return -EINVAL;
     if (rows == 0) return 0;
-    if (!verify_sizes_ok(rows, vocab)) return -EINVAL;
+    if (rows >= (1u << 22) || vocab == 0 || vocab >= (1ull << 31)) return -EINVAL;    // 1,024 threads a request
     if (!q_start || !aligned4(q_start) || !count || !aligned4(count) || !next || !aligned4(next) || !status)
         return -EINVAL;
     const uintptr_t in_row = type == DMADESC_KV_FP32 ? 3u : 1u;
@@ -559,9 +545,8 @@ int dmadesc_verify_drafts(const void *probs, int64_t probs_stride, const void *d
                       !aligned4(tokens) || !parent || !aligned4(parent) || !u || !aligned4(u) || !path ||
                       !aligned4(path)))
         return -EINVAL;
-    if (!ws_ok(ws, ws_bytes, dd::ws_verify(total, rows, vocab))) return -EINVAL;
     dd::VerifyArgs a{probs, draft, probs_stride, draft_stride, type, vocab, tokens, parent, q_start, rows,
-                     total, u, path, count, next, status, ws};
+                     total, u, path, count, next, status};
     return launched(dd::launch_verify(a, static_cast<hipStream_t>(stream)));
 }
 

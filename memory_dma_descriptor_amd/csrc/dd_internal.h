@@ -150,7 +150,6 @@ struct VerifyArgs {
     const float *u;
     int32_t *path, *count, *next;
     uint8_t *status;
-    void *ws;
 };
 
 struct KvPageArgs {
@@ -211,8 +210,6 @@ hipError_t launch_kv_read_check(const dmadesc_kv_cache &c, const int32_t *first,
 uint64_t kv_keep_groups(uint32_t rows, uint32_t kv_heads);
 hipError_t launch_kv_keep(const KvKeepArgs &a, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs &a, hipStream_t s);
-uint64_t verify_groups(uint32_t rows, uint64_t vocab);
-size_t ws_verify(uint64_t total, uint32_t rows, uint64_t vocab);
 hipError_t launch_kv_free(const KvPageArgs &k, const int32_t *row, const int32_t *keep,
                           hipStream_t s);
 hipError_t launch_kv_fork(const KvPageArgs &k, const int32_t *parent, const int32_t *child,

@@ -12,12 +12,14 @@
 // remainder is p without the tokens refused. Everything is f64: the answers are
 // whole numbers, so that what is summed in another order must not change them.
 //
-// Two launches. The first walks the tree, one workgroup a request: a test reads
-// two numbers, all of them gathered beforehand, and a mass W is summed only where
-// a child follows a refused one. The second draws the token after the last
-// accepted one: workgroups sum 4,096 weights each, and a request's last one to
-// finish looks for the place where the running sum passes u W. The sums are added
-// in one order whoever is last.
+// One workgroup a request, one launch. The walk's tests read two numbers each,
+// gathered for all nodes at once, and a first child's test depends on nothing
+// else; one wave walks, and all sum a mass W where a child follows a refused one.
+// Then the weights of the last node are summed in 64 even parts, four of a wave,
+// and one wave looks for the place where the running sum passes u W: for the
+// part, for the 64th of it, for the weight.
+#include <type_traits>
+
 #include "dd_internal.h"
 #include "dd_kv.hpp"
 
@@ -25,97 +27,342 @@ namespace dd {
 namespace {
 
 constexpr int kMost = (int)DMADESC_TREE_MOST;
-constexpr int kWalkThreads = 1024;
-constexpr int kDrawThreads = 256;
-constexpr int kPer = 16;                                // weights of a thread
-constexpr uint32_t kTile = kDrawThreads * kPer;
-
-// What the draw of a request needs from its walk.
-struct Draw {
-    double c, c_before;         // the remainder, and the one before the last refusal
-    int64_t row;                // of probs and draft; -1: nothing is drawn
-    int32_t refused, last;      // tokens refused there; the last one of them
-    float u;
-    uint32_t done;              // workgroups that have summed their part
-};
+constexpr int kThreads = 1024;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kOwn = 4;                                 // parts of a wave
+constexpr int kParts = kOwn * kWaves;
+constexpr uint32_t kLongPart = kWave * kWave;           // weights of a part that a wave finishes alone
+constexpr int kBits = 1 << 14;                          // of the refused tokens, by runs of a load
 
 struct Args {
     const void *probs, *draft;
     int64_t probs_row, draft_row;
-    uint64_t vocab;
+    uint32_t vocab;                                     // < 2^31, so that places past it still fit
     const int32_t *tokens, *parent, *q_start;
-    uint32_t rows, total, tiles;
+    uint32_t rows, total;
     const float *u;
     int32_t *path, *count, *next;
     uint8_t *status;
-    Draw *draw;                 // [rows]
-    int32_t *refused;           // [total] refused tokens of the last node, from q_start on
-    double2 *part;              // [rows][tiles] mass of the remainder and of the one before
 };
 
-// The numbers of a row; what is not positive and finite counts as 0.
+// The tokens refused at a node; without a draft row, also a bit for each run of
+// numbers that a load takes, which says where to look the list up.
+struct Refused {
+    int32_t token[kMost];
+    uint32_t bits[kBits / 32];
+};
+
+constexpr int kN = 4;                                   // numbers that a thread loads at once
+
+// What is negative or NaN counts as 0, infinity as the largest number.
+__device__ __forceinline__ float sound(float x) { return __builtin_amdgcn_fmed3f(x, 0.0f, 3.402823466e38f); }
+
 template <int kType>
-__device__ __forceinline__ float sound(const void *p, int64_t at)
+__device__ __forceinline__ float number(const void *p, int64_t at)
 {
     float x;
     if constexpr (kType == DMADESC_KV_FP32) x = static_cast<const float *>(p)[at];
     else if constexpr (kType == DMADESC_KV_BF16) x = __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[at] << 16);
     else x = (float)static_cast<const _Float16 *>(p)[at];
-    return x > 0.0f && x < __builtin_inff() ? x : 0.0f;
+    return sound(x);
 }
 
-// kN consecutive numbers from `at` on, zeros past `end`.
-template <int kType, int kN>
-__device__ __forceinline__ void sound_run(const void *p, int64_t row, uint64_t at, uint64_t end, float (&x)[kN])
-{
-    if (at + kN <= end) {
-        if constexpr (kType == DMADESC_KV_FP32) {
-            float y[kN];
-            __builtin_memcpy(y, static_cast<const float *>(p) + row + at, sizeof y);
-#pragma unroll
-            for (int i = 0; i < kN; ++i) x[i] = y[i];
-        } else {
-            uint16_t y[kN];
-            __builtin_memcpy(y, static_cast<const uint16_t *>(p) + row + at, sizeof y);
-#pragma unroll
-            for (int i = 0; i < kN; ++i)
-                x[i] = kType == DMADESC_KV_BF16 ? __uint_as_float((uint32_t)y[i] << 16) : (float)__builtin_bit_cast(_Float16, y[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] = x[i] > 0.0f && x[i] < __builtin_inff() ? x[i] : 0.0f;
-    } else {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] = at + i < end ? sound<kType>(p, row + (int64_t)(at + i)) : 0.0f;
+// kN numbers as they lie in memory, at any place.
+template <int kType>
+struct Raw {
+    typedef typename std::conditional<kType == DMADESC_KV_FP32, uint32_t, uint16_t>::type Bits;
+    uint32_t w[kN * sizeof(Bits) / 4];
+
+    __device__ __forceinline__ void load(const void *p, int64_t at)
+    {
+        __builtin_memcpy(w, static_cast<const Bits *>(p) + at, sizeof w);
     }
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (kType == DMADESC_KV_FP32) return sound(__uint_as_float(w[i]));
+        else if constexpr (kType == DMADESC_KV_BF16)
+            return sound(__uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16));
+        else return sound((float)__builtin_bit_cast(_Float16, (uint16_t)(w[i / 2] >> (16 * (i & 1)))));
+    }
+};
+
+// Sums across lanes through the vector unit's own lane moves (a step takes some
+// 30 cycles; the shuffles of dd_device.hpp, which pass through LDS, 150).
+template <int kCtrl, int kRowMask = 0xf>
+__device__ __forceinline__ double moved(double x)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, kCtrl, kRowMask, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), kCtrl, kRowMask, 0xf, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-template <int kThreads>
-__device__ __forceinline__ double block_sum(double v, double *scratch)
+// Inclusive running sum across the wave: rows of 16 lanes, then their ends.
+__device__ __forceinline__ double running_sum(double x)
 {
-    v = wave_sum(v);
-    __syncthreads();
-    if (lane() == 0) scratch[wave()] = v;
-    __syncthreads();
-    double all = 0.0;
-#pragma unroll
-    for (int k = 0; k < kThreads / kWave; ++k) all += scratch[k];
-    return all;
+    x += moved<0x111>(x);               // from 1, 2, 4 and 8 lanes to the left in the row
+    x += moved<0x112>(x);
+    x += moved<0x114>(x);
+    x += moved<0x118>(x);
+    x += moved<0x142, 0xa>(x);          // lane 15 to row 1, 47 to row 3
+    x += moved<0x143, 0xc>(x);          // lane 31 to rows 2 and 3
+    return x;
 }
+
+// The sum of a row of 16 lanes, in all of them.
+__device__ __forceinline__ double row_sum(double x)
+{
+    x += moved<0x128>(x);               // turned by 8, 4, 2, 1
+    x += moved<0x124>(x);
+    x += moved<0x122>(x);
+    x += moved<0x121>(x);
+    return x;
+}
+
+__device__ __forceinline__ double lane_value(double x, int from)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, from);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), from);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Whether a lane's condition holds, where it is the same in all lanes.
+__device__ __forceinline__ bool uniform(bool x) { return __ballot(x) != 0; }
 
 __device__ __forceinline__ double remains(float p, float d, double c)
 {
-    const double w = (double)p - c * (double)d;
-    return w > 0.0 ? w : 0.0;
+    return __builtin_fmax((double)p - c * (double)d, 0.0);      // (all finite)
+}
+
+// What is drawn from: a row of probs and of draft, c, and the refused tokens.
+struct Row {
+    int64_t p, d;
+    double c;
+    int refused;                                        // of the list; without a draft row
+};
+
+// A run of kN weights.
+template <int kType, bool kDraft>
+struct Run {
+    Raw<kType> p, d;
+
+    __device__ __forceinline__ void load(const Args &a, const Row &w, int64_t at)
+    {
+        p.load(a.probs, w.p + at);
+        if constexpr (kDraft) d.load(a.draft, w.d + at);
+    }
+    // Their sum, of places lo .. hi - 1 of the row if `part`; the run starts at `at`.
+    __device__ __forceinline__ double sum(const Row &w, const Refused &no, uint32_t at, bool part, uint32_t lo,
+                                          uint32_t hi) const
+    {
+        double x[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i] = kDraft ? remains(p.get(i), d.get(i), w.c) : (double)p.get(i);
+        if (part) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) x[i] = at + i >= lo && at + i < hi ? x[i] : 0.0;
+        }
+        if constexpr (!kDraft) {
+            if (w.refused > 0) {
+                const uint32_t bit = lo / kN & (kBits - 1);
+                if (no.bits[bit / 32] >> (bit & 31) & 1u)
+                    for (int k = 0; k < w.refused; ++k) {
+                        const uint32_t y = (uint32_t)no.token[k] - at;
+#pragma unroll
+                        for (int i = 0; i < kN; ++i) x[i] = y == (uint32_t)i ? 0.0 : x[i];
+                    }
+            }
+        }
+        return (x[0] + x[1]) + (x[2] + x[3]);
+    }
+};
+
+// One weight, of any row length.
+template <int kType, bool kDraft>
+__device__ __forceinline__ double weight(const Args &a, const Row &w, const Refused &no, uint32_t at)
+{
+    const float p = number<kType>(a.probs, w.p + at);
+    if constexpr (kDraft) return remains(p, number<kType>(a.draft, w.d + at), w.c);
+    bool out = false;
+    for (int k = 0; k < w.refused; ++k) out |= (uint32_t)no.token[k] == at;
+    return out ? 0.0 : (double)p;
+}
+
+// Masses of the kParts parts of [from, end), `part` weights each (a multiple of a
+// wave's loads), in masses[]. Called by the whole workgroup.
+template <int kType, bool kDraft>
+__device__ __forceinline__ void sum_parts(const Args &a, const Row &w, const Refused &no, uint32_t from, uint32_t end,
+                                          uint32_t part, double *masses)
+{
+    const int ln = lane();
+    double sum[kOwn] = {};
+    const uint32_t start = from + (uint32_t)__builtin_amdgcn_readfirstlane(wave()) * kOwn * part;
+    typedef Run<kType, kDraft> R;
+    if (a.vocab < (uint32_t)kN) {
+        if (start + ln < end) sum[0] = weight<kType, kDraft>(a, w, no, start + ln);
+    } else if (start + kOwn * part <= end) {
+        // The next loads are in flight under this round's sums.
+        R now[kOwn], next[kOwn];
+        const uint32_t own = (uint32_t)ln * kN;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) now[i].load(a, w, (int64_t)(start + i * part) + own);
+        for (uint32_t k = 0; k < part; k += kWave * kN) {
+            const uint32_t after = k + kWave * kN < part ? k + kWave * kN : k;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) next[i].load(a, w, (int64_t)(start + i * part + after) + own);
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                const uint32_t at = start + i * part + k + own;
+                sum[i] += now[i].sum(w, no, at, false, at, end);
+                now[i] = next[i];
+            }
+        }
+    } else if (start < end) {
+        // The wave with the row's end: a run that would pass it is moved back, and
+        // counts from its own place on (`end` is the row's or a multiple of kN).
+        for (uint32_t k = 0; k < part; k += kWave * kN) {
+            R run[kOwn];
+            uint32_t at[kOwn];
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                at[i] = start + i * part + k + (uint32_t)ln * kN;
+                run[i].load(a, w, at[i] < a.vocab - kN ? at[i] : a.vocab - kN);
+            }
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i)
+                sum[i] += run[i].sum(w, no, at[i] < a.vocab - kN ? at[i] : a.vocab - kN, true, at[i], end);
+        }
+    }
+    // Lane 16 i ends up with the sum of part i.
+    static_assert(kOwn == 4);
+    const bool up = ln & 32, odd = ln & 16;
+    const double s0 = (up ? sum[2] : sum[0]) + __shfl_xor(up ? sum[0] : sum[2], 32, kWave);
+    const double s1 = (up ? sum[3] : sum[1]) + __shfl_xor(up ? sum[1] : sum[3], 32, kWave);
+    const double s = row_sum((odd ? s1 : s0) + __shfl_xor(odd ? s0 : s1, 16, kWave));
+    __syncthreads();
+    if ((ln & 15) == 0) masses[wave() * kOwn + ln / 16] = s;
+    __syncthreads();
+}
+
+// Weights of a part when kParts of them hold n.
+__device__ __forceinline__ uint32_t part_of(uint32_t n)
+{
+    constexpr uint32_t kStep = kWave * kN;
+    return ((n + kParts - 1) / kParts + kStep - 1) / kStep * kStep;
+}
+
+// The walk, of one wave: where it stands between two masses.
+struct Walk {
+    int v, kids_at, cnt, refused;       // node, its next child to look at, accepted rows, refused children
+    double c, c_before, W, Q;
+    bool pending;                       // c is new, its mass not summed yet
+
+    __device__ __forceinline__ void start()
+    {
+        c = c_before = 0.0;
+        W = Q = 1.0;
+        pending = false;
+    }
+};
+
+constexpr uint32_t kFirst = 1u << 16, kFit = 1u << 17;  // of a node: accepted if tried first; can be tried
+
+// Goes on until a mass is wanted (true) or no child is accepted. The whole numbers
+// are scalars: what they come from is the same in all lanes, which the compiler
+// does not see everywhere.
+template <bool kDraft>
+__device__ __forceinline__ bool walk(Walk &s, int n, const uint32_t *node, const int32_t *tok, const float *px,
+                                     const float *dx, const float *ux, int32_t *path, int32_t *gone)
+{
+    const int ln = lane();
+    int v = __builtin_amdgcn_readfirstlane(s.v), kids_at = __builtin_amdgcn_readfirstlane(s.kids_at);
+    int cnt = __builtin_amdgcn_readfirstlane(s.cnt), refused = __builtin_amdgcn_readfirstlane(s.refused);
+    bool wants = false;
+    for (;;) {
+        int taken = -1;
+        for (int k = kids_at & -kWave; k < n; k += kWave) {
+            const uint32_t me = k + ln < n ? node[k + ln] : 0u;
+            const uint64_t first = __ballot((me & kFirst) != 0);
+            const uint32_t up = (me & kFit) && k + ln >= kids_at ? me & 0xffffu : 0xfffeu;
+            uint64_t kids = __ballot(up == (uint32_t)v);
+            if (refused == 0 && n <= kWave) {
+                // As long as first children are accepted, a look at the lanes takes each.
+                while (kids != 0 && (first >> (__ffsll((unsigned long long)kids) - 1) & 1)) {
+                    v = __ffsll((unsigned long long)kids) - 1;
+                    if (ln == 0) path[cnt] = v;
+                    ++cnt;
+                    kids = __ballot(up == (uint32_t)v);
+                }
+            }
+            while (kids != 0) {
+                const int at = __ffsll((unsigned long long)kids) - 1, j = k + at;
+                kids &= kids - 1;
+                bool yes;
+                if (refused == 0) {
+                    yes = first >> at & 1;
+                } else {
+                    const int x = tok[j];
+                    bool again = false;
+                    for (int i = 0; i < refused; i += kWave) again |= i + ln < refused && gone[i + ln] == x;
+                    if (uniform(again)) continue;
+                    if constexpr (kDraft) {
+                        if (uniform(!(s.Q > 0.0))) continue;
+                        if (uniform(s.pending)) {
+                            kids_at = j;
+                            wants = true;
+                            break;
+                        }
+                        yes = uniform((double)ux[j] * (double)dx[j] * s.W < remains(px[j], dx[j], s.c) * s.Q);
+                    } else {
+                        yes = uniform((double)ux[j] * s.W < (double)px[j]);
+                    }
+                }
+                if (yes) {
+                    taken = j;
+                    break;
+                }
+                if (ln == 0) gone[refused] = tok[j];
+                ++refused;
+                if constexpr (kDraft) {
+                    s.c_before = s.c;
+                    s.c += s.W / s.Q;
+                    s.Q -= (double)dx[j];
+                    s.pending = true;
+                } else {
+                    s.W -= (double)px[j];
+                }
+            }
+            if (wants || taken >= 0) break;
+        }
+        if (wants || taken < 0) break;
+        v = taken;
+        kids_at = v + 1;
+        if (ln == 0) path[cnt] = v;
+        ++cnt;
+        refused = 0;
+        s.start();
+    }
+    s.v = v;
+    s.kids_at = kids_at;
+    s.cnt = cnt;
+    s.refused = refused;
+    return wants;
 }
 
 template <int kType, bool kDraft>
-__global__ __launch_bounds__(kWalkThreads) void k_verify_walk(Args a)
+__global__ __launch_bounds__(kThreads) void k_verify(Args a)
 {
-    __shared__ int16_t up[kMost];
-    __shared__ int32_t tok[kMost], path[kMost], gone[kMost];
+    static_assert(kParts == kWave);
+    __shared__ uint32_t node[kMost];
+    __shared__ int32_t tok[kMost], path[kMost];
     __shared__ float px[kMost], dx[kMost], ux[kMost];
-    __shared__ double scratch[kWalkThreads / kWave];
+    __shared__ double masses[kParts];
     __shared__ uint32_t wrong;
+    __shared__ Refused gone;
+    __shared__ int shared_v, shared_cnt, shared_refused;
+    __shared__ double shared_c[2];                      // the remainder's c, and the one before
+    __shared__ bool more;
     const uint32_t b = blockIdx.x;
     const int tid = (int)threadIdx.x, ln = lane();
     uint32_t s0, s1;
@@ -125,312 +372,159 @@ __global__ __launch_bounds__(kWalkThreads) void k_verify_walk(Args a)
                  (b == a.rows - 1 && raw1 != a.total) || s1 - s0 > (uint32_t)kMost;
     const int n = inval ? 0 : (int)(s1 - s0);
     if (tid == 0) wrong = 0;
+    if (!kDraft && tid < kBits / 32) gone.bits[tid] = 0;
     __syncthreads();
     if (tid < n) {
         const int64_t row = (int64_t)s0 + tid;
         int p = tid == 0 ? -1 : a.parent[row];
+        const int t = a.tokens[row];
+        const float u = a.u[row];
         if (p < -1 || p >= tid) {
             if (tid > 0) wrong = 1;                     // every writer writes 1
             p = -1;
         }
-        const int t = a.tokens[row];
-        up[tid] = (int16_t)p;
+        const bool on = p >= 0 && t >= 0 && (uint32_t)t < a.vocab;
+        const float pv = on ? number<kType>(a.probs, (int64_t)(s0 + p) * a.probs_row + t) : 0.0f;
+        const float dv = kDraft && on ? number<kType>(a.draft, (int64_t)(s0 + p) * a.draft_row + t) : 0.0f;
+        const bool fit = kDraft ? dv > 0.0f : pv > 0.0f;
+        const bool first = kDraft ? (double)u * (double)dv < (double)pv : u < pv;
+        node[tid] = ((uint32_t)p & 0xffffu) | (first ? kFirst : 0u) | (fit ? kFit : 0u);
         tok[tid] = t;
-        ux[tid] = a.u[row];
-        const bool on = p >= 0 && t >= 0 && (uint64_t)t < a.vocab;
-        px[tid] = on ? sound<kType>(a.probs, (int64_t)(s0 + p) * a.probs_row + t) : 0.0f;
-        dx[tid] = kDraft && on ? sound<kType>(a.draft, (int64_t)(s0 + p) * a.draft_row + t) : 0.0f;
+        px[tid] = pv;
+        dx[tid] = dv;
+        ux[tid] = u;
+        if (tid == 0) path[0] = 0;
     }
     __syncthreads();
     inval = inval || wrong;
-
-    int cnt = 0;
-    int64_t row = -1;
-    double c = 0.0, c_before = 0.0;
-    int refused = 0, last = -1;
-    if (!inval && n > 0) {
-        int v = 0;
-        if (tid == 0) path[0] = 0;
-        cnt = 1;
-        for (;;) {                                      // down the tree: a child comes after its parent
-            double W = 1.0, Q = 1.0;
-            bool pending = false;                       // c is new, its mass not summed yet
-            int taken = -1;
-            c = c_before = 0.0;
-            refused = 0;
-            last = -1;
-            for (int k = v / kWave * kWave; k < n && taken < 0; k += kWave) {
-                uint64_t kids = __ballot(k + ln < n && k + ln > v && up[k + ln < n ? k + ln : 0] == v);
-                while (kids && taken < 0) {
-                    const int j = k + __ffsll((unsigned long long)kids) - 1;
-                    kids &= kids - 1;
-                    const int x = tok[j];
-                    const double u = ux[j], p = px[j], d = dx[j];
-                    bool again = false;
-                    for (int i = 0; i < refused; i += kWave) again |= i + ln < refused && gone[i + ln] == x;
-                    if (__ballot(again)) continue;
-                    if constexpr (kDraft) {
-                        if (!(d > 0.0 && Q > 0.0)) continue;
-                        if (pending) {                  // the mass that the last refusal left
-                            double sum = 0.0;
-                            for (uint64_t at = (uint64_t)tid * 4; at < a.vocab; at += kWalkThreads * 4) {
-                                float pv[4], dv[4];
-                                sound_run<kType>(a.probs, (int64_t)(s0 + v) * a.probs_row, at, a.vocab, pv);
-                                sound_run<kType>(a.draft, (int64_t)(s0 + v) * a.draft_row, at, a.vocab, dv);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) sum += remains(pv[i], dv[i], c);
-                            }
-                            sum = block_sum<kWalkThreads>(sum, scratch);
-                            pending = false;
-                            if (sum > 0.0) W = sum;
-                            else c = c_before;          // nothing would be left: it stays as it was
-                        }
-                        if (u * d * W < remains((float)p, (float)d, c) * Q) {
-                            taken = j;
-                            break;
-                        }
-                        c_before = c;
-                        c += W / Q;
-                        Q -= d;
-                        pending = true;
-                    } else {
-                        if (!(p > 0.0)) continue;
-                        if (u * W < p) {
-                            taken = j;
-                            break;
-                        }
-                        W -= p;
-                        last = x;
-                    }
-                    __syncthreads();                    // every wave has read the list
-                    if (tid == 0) gone[refused] = x;
-                    ++refused;
-                    __syncthreads();
-                }
-            }
-            row = (int64_t)s0 + v;
-            if (taken < 0) break;
-            v = taken;
-            if (tid == 0) path[cnt] = v;
-            ++cnt;
-        }
-    }
-    __syncthreads();
-    for (uint32_t i = tid; i < s1 - s0; i += kWalkThreads) a.path[s0 + i] = (int)i < cnt ? path[i] : -1;
-    if (!kDraft)
-        for (int i = tid; i < refused; i += kWalkThreads) a.refused[s0 + i] = gone[i];
-    if (tid == 0) {
-        a.count[b] = cnt;
-        a.status[b] = inval ? DMADESC_KV_EINVAL : DMADESC_KV_OK;
-        if (row < 0) a.next[b] = -1;
-        a.draw[b] = Draw{c, c_before, row, refused, last, row < 0 ? 0.0f : ux[0], 0u};
-    }
-}
-
-// The weights of kN tokens from `at` on: of the remainder and of the one before.
-template <int kType, bool kDraft, int kN>
-__device__ __forceinline__ void weights(const Args &a, const Draw &w, const int32_t *gone, uint64_t at, uint64_t end,
-                                        double (&now)[kN], double (&before)[kN])
-{
-    float p[kN], d[kN];
-    sound_run<kType>(a.probs, w.row * a.probs_row, at, end, p);
-    if constexpr (kDraft) {
-        sound_run<kType>(a.draft, w.row * a.draft_row, at, end, d);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            now[i] = remains(p[i], d[i], w.c);
-            before[i] = remains(p[i], d[i], w.c_before);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) now[i] = before[i] = p[i];
-        for (int k = 0; k < w.refused; ++k) {
-            const uint64_t x = (uint64_t)gone[k] - at;
-#pragma unroll
-            for (int i = 0; i < kN; ++i)
-                if (x == (uint64_t)i) {
-                    now[i] = 0.0;
-                    if (gone[k] != w.last) before[i] = 0.0;
-                }
-        }
-    }
-}
-
-template <int kType, bool kDraft>
-__global__ __launch_bounds__(kDrawThreads) void k_verify_draw(Args a)
-{
-    __shared__ double scratch[kDrawThreads / kWave];
-    __shared__ uint32_t is_last, tile_at, token_at, some_at;
-    __shared__ int32_t gone[kDraft ? 1 : kMost];
-    const uint32_t b = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
-    const int tid = (int)threadIdx.x;
-    const Draw w = a.draw[b];
-    if (w.row < 0) return;
-    if (!kDraft) {
-        const uint32_t s0 = (uint32_t)a.q_start[b];
-        for (int i = tid; i < w.refused; i += kDrawThreads) gone[i] = a.refused[s0 + i];
-        __syncthreads();
-    }
-    {
-        const uint64_t from = (uint64_t)tile * kTile, end = from + kTile < a.vocab ? from + kTile : a.vocab;
-        double now = 0.0, before = 0.0;
-#pragma unroll
-        for (int k = 0; k < kPer / 4; ++k) {
-            const uint64_t at = from + (uint64_t)(k * kDrawThreads + tid) * 4;
-            if (at >= end) break;
-            double x[4], y[4];
-            weights<kType, kDraft>(a, w, gone, at, end, x, y);
-            now += (x[0] + x[1]) + (x[2] + x[3]);
-            before += (y[0] + y[1]) + (y[2] + y[3]);
-        }
-        now = block_sum<kDrawThreads>(now, scratch);
-        before = block_sum<kDrawThreads>(before, scratch);
+    if (inval || n == 0) {
+        for (uint32_t i = tid; i < s1 - s0; i += kThreads) a.path[s0 + i] = -1;
         if (tid == 0) {
-            double2 *const p = &a.part[(uint64_t)b * a.tiles + tile];
-            __hip_atomic_store(&p->x, now, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __hip_atomic_store(&p->y, before, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            is_last = __hip_atomic_fetch_add(&a.draw[b].done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-                      a.tiles - 1;
-            tile_at = token_at = some_at = 0xffffffffu;
+            a.count[b] = 0;
+            a.status[b] = inval ? DMADESC_KV_EINVAL : DMADESC_KV_OK;
+            a.next[b] = -1;
         }
-        __syncthreads();
-        if (!is_last) return;
-    }
-    // The request's last workgroup: all parts are there. Their running sum first.
-    const double2 *const part = a.part + (uint64_t)b * a.tiles;
-    auto part_of = [&](uint32_t t, bool use_before) {
-        const double *const p = use_before ? &part[t].y : &part[t].x;
-        return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    };
-    double all = 0.0, all_before = 0.0;
-    for (uint32_t t = tid; t < a.tiles; t += kDrawThreads) {
-        all += part_of(t, false);
-        all_before += part_of(t, true);
-    }
-    all = block_sum<kDrawThreads>(all, scratch);
-    all_before = block_sum<kDrawThreads>(all_before, scratch);
-    const bool use_before = !(all > 0.0);                   // nothing is left: the remainder before
-    if (use_before) all = all_before;
-    if (!(all > 0.0)) {
-        if (tid == 0) a.next[b] = -1;
         return;
     }
-    const double aim = (double)w.u * all;
-    // The first part whose running sum passes the aim; else the last that has any mass.
-    double run = 0.0;
-    uint32_t some = 0;
-    double some_run = 0.0;
-    for (uint32_t t0 = 0; t0 < a.tiles && tile_at == 0xffffffffu; t0 += kDrawThreads) {
-        const uint32_t t = t0 + tid;
-        const double mine = t < a.tiles ? part_of(t, use_before) : 0.0;
-        double sum;
-        const double at = run + block_excl_scan<kDrawThreads, double>(mine, scratch, &sum);
-        if (mine > 0.0 && at + mine > aim) atomicMin(&tile_at, t);
-        if (mine > 0.0) {
-            some = t;
-            some_run = at;
-        }
-        run += sum;
-        __syncthreads();
-    }
-    // (A u of 1 or more, or NaN, or the sums' last bits: no part passes.)
-    const bool none = tile_at == 0xffffffffu;
-    if (none) {
-        if (tid == 0) tile_at = 0;
-        __syncthreads();
-        atomicMax(&tile_at, some);
-        __syncthreads();
-    }
-    const uint32_t at_tile = tile_at;
-    {
-        const uint64_t from = (uint64_t)at_tile * kTile, end = from + kTile < a.vocab ? from + kTile : a.vocab;
-        // The mass before this part, in the same order as above.
-        double ahead = 0.0;
-        for (uint32_t t = tid; t < at_tile; t += kDrawThreads) ahead += part_of(t, use_before);
-        ahead = block_sum<kDrawThreads>(ahead, scratch);
-        (void)some_run;
-        double x[kPer], y[kPer];
-        const uint64_t at = from + (uint64_t)tid * kPer;
-        if (at < end) {
-            weights<kType, kDraft>(a, w, gone, at, end, x, y);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) x[i] = y[i] = 0.0;
-        }
-        double mine = 0.0, sum;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (use_before) x[i] = y[i];
-            mine += x[i];
-        }
-        double upto = ahead + block_excl_scan<kDrawThreads, double>(mine, scratch, &sum);
-        int hit = -1, any = -1;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            upto += x[i];
-            if (x[i] > 0.0) {
-                if (hit < 0 && upto > aim) hit = i;
-                any = i;
-            }
-        }
-        if (tid == 0) some_at = 0;
-        __syncthreads();
-        if (hit >= 0 && !none) atomicMin(&token_at, (uint32_t)(tid * kPer + hit));
-        if (any >= 0) atomicMax(&some_at, (uint32_t)(tid * kPer + any));
-        __syncthreads();
-        if (tid == 0) a.next[b] = (int32_t)(from + (token_at != 0xffffffffu ? token_at : some_at));
-    }
-}
 
-template <int kType, bool kDraft>
-void launch_both(const Args &a, hipStream_t s)
-{
-    k_verify_walk<kType, kDraft><<<a.rows, kWalkThreads, 0, s>>>(a);
-    k_verify_draw<kType, kDraft><<<a.rows * a.tiles, kDrawThreads, 0, s>>>(a);
+    // (The walk's state field by field: copied whole, the compiler puts it into LDS by
+    // thread number, which it reads from the dispatch packet in host memory: 3 to 7 us.)
+    Walk s;
+    s.v = s.refused = 0;
+    s.kids_at = s.cnt = 1;
+    s.start();
+    auto row_of = [&](int refused) {                    // the row that the walk has come to
+        const int64_t row = (int64_t)s0 + __builtin_amdgcn_readfirstlane(shared_v);
+        return Row{row * a.probs_row, row * a.draft_row, lane_value(shared_c[0], 0), refused};
+    };
+    for (;;) {
+        if (__builtin_amdgcn_readfirstlane(wave()) == 0) {
+            const bool wants = walk<kDraft>(s, n, node, tok, px, dx, ux, path, gone.token);
+            if (ln == 0) {
+                shared_v = s.v;
+                shared_cnt = s.cnt;
+                shared_refused = s.refused;
+                shared_c[0] = s.c;
+                shared_c[1] = s.c_before;
+                more = wants;
+            }
+            if (!kDraft && !wants)
+                for (int i = ln; i < s.refused; i += kWave) {
+                    const uint32_t bit = (uint32_t)gone.token[i] / kN & (kBits - 1);
+                    atomicOr(&gone.bits[bit / 32], 1u << (bit & 31));
+                }
+        }
+        __syncthreads();
+        if (!kDraft || !__builtin_amdgcn_readfirstlane(more)) break;
+        const Row w = row_of(0);
+        sum_parts<kType, kDraft>(a, w, gone, 0, a.vocab, part_of(a.vocab), masses);
+        const double mass = lane_value(running_sum(masses[ln]), kWave - 1);
+        s.pending = false;
+        if (uniform(mass > 0.0)) s.W = mass;
+        else s.c = s.c_before;                          // nothing would be left: it stays as it was
+    }
+    const int refused = __builtin_amdgcn_readfirstlane(shared_refused);
+    for (int i = tid; i < n; i += kThreads) a.path[s0 + i] = i < shared_cnt ? path[i] : -1;
+    if (tid == 0) {
+        a.count[b] = shared_cnt;
+        a.status[b] = DMADESC_KV_OK;
+    }
+
+    // The next token, from what remains of row v.
+    Row w = row_of(refused);
+    uint32_t from = 0, end = a.vocab, part = part_of(end);
+    double aim = 0.0, ahead = 0.0;                      // u times the mass; mass before `from`
+    bool whole = true, past = false;                    // past: no running sum passes the aim, so the last weight
+    for (;;) {
+        double mine = 0.0;                              // of the lane's 64th of [from, end)
+        if (part > 1) {
+            if (whole || part * kParts > kLongPart) {   // by the whole workgroup, until a part is short
+                sum_parts<kType, kDraft>(a, w, gone, from, end, part, masses);
+                mine = masses[ln];
+            } else {
+                const uint32_t at = from + (uint32_t)ln * part, to = at + part < end ? at + part : end;
+                if (a.vocab < (uint32_t)kN) {
+                    for (uint32_t k = at; k < to; ++k) mine += weight<kType, kDraft>(a, w, gone, k);
+                } else {                                // (from and part are multiples of kN)
+#pragma unroll 4
+                    for (uint32_t k = at; k < to; k += kN) {
+                        Run<kType, kDraft> run;
+                        const uint32_t place = k < a.vocab - kN ? k : a.vocab - kN;
+                        run.load(a, w, place);
+                        mine += run.sum(w, gone, place, true, k, to);
+                    }
+                }
+            }
+        } else if (from + ln < end) {
+            mine = weight<kType, kDraft>(a, w, gone, from + ln);
+        }
+        const double upto = running_sum(mine);
+        if (whole) {
+            const double all = lane_value(upto, kWave - 1);
+            if (uniform(!(all > 0.0))) {
+                if (w.refused < refused || refused == 0) {      // nothing to draw from
+                    if (tid == 0) a.next[b] = -1;
+                    return;
+                }
+                w.c = lane_value(shared_c[1], 0);                      // nothing remains: the remainder before
+                w.refused = refused - 1;
+                continue;
+            }
+            aim = (double)ux[0] * all;
+            whole = false;
+        }
+        // The first part whose running sum passes the aim. Where none does (the sums'
+        // last bits, or u of 1 or more, or NaN) it is the last with any mass.
+        const uint64_t some = __ballot(mine > 0.0), pass = __ballot(mine > 0.0 && ahead + upto > aim);
+        past = past || pass == 0;
+        const int k = past ? 63 - __clzll((unsigned long long)some) : __ffsll((unsigned long long)pass) - 1;
+        ahead += lane_value(upto - mine, k);
+        from += (uint32_t)k * part;
+        if (part == 1) break;
+        end = from + part < end ? from + part : end;
+        if (part > kLongPart) {
+            part = part_of(part);
+        } else {                                        // one wave finishes
+            if (__builtin_amdgcn_readfirstlane(wave()) != 0) return;
+            part = part > kWave ? (part + kWave - 1) / kWave : 1;
+        }
+    }
+    if (tid == 0) a.next[b] = (int32_t)from;
 }
 
 template <int kType>
 void launch_type(const Args &a, hipStream_t s)
 {
-    if (a.draft) launch_both<kType, true>(a, s);
-    else launch_both<kType, false>(a, s);
-}
-
-struct Layout {
-    size_t refused, part, bytes;
-    uint64_t tiles;
-};
-
-Layout layout_of(uint64_t total, uint32_t rows, uint64_t vocab)
-{
-    Layout l{};
-    l.tiles = (vocab + kTile - 1) / kTile;
-    l.refused = align256(sizeof(Draw) * (size_t)rows);
-    l.part = l.refused + align256(4 * total);
-    l.bytes = l.part + align256(sizeof(double2) * (size_t)rows * l.tiles);
-    return l;
+    if (a.draft) k_verify<kType, true><<<a.rows, kThreads, 0, s>>>(a);
+    else k_verify<kType, false><<<a.rows, kThreads, 0, s>>>(a);
 }
 
 }  // namespace
 
-uint64_t verify_groups(uint32_t rows, uint64_t vocab)
-{
-    return rows * layout_of(0, rows, vocab).tiles;
-}
-
-size_t ws_verify(uint64_t total, uint32_t rows, uint64_t vocab)
-{
-    return layout_of(total, rows, vocab).bytes;
-}
-
 hipError_t launch_verify(const VerifyArgs &v, hipStream_t s)
 {
-    const Layout l = layout_of(v.total, v.rows, v.vocab);
-    uint8_t *const ws = static_cast<uint8_t *>(v.ws);
-    Args a{v.probs, v.draft, v.probs_row, v.draft_row, v.vocab, v.tokens, v.parent, v.q_start, v.rows,
-           (uint32_t)v.total, (uint32_t)l.tiles, v.u, v.path, v.count, v.next, v.status,
-           reinterpret_cast<Draw *>(ws), reinterpret_cast<int32_t *>(ws + l.refused),
-           reinterpret_cast<double2 *>(ws + l.part)};
+    const Args a{v.probs, v.draft, v.probs_row, v.draft_row, (uint32_t)v.vocab, v.tokens, v.parent, v.q_start, v.rows,
+                 (uint32_t)v.total, v.u, v.path, v.count, v.next, v.status};
     if (v.type == DMADESC_KV_BF16) launch_type<DMADESC_KV_BF16>(a, s);
     else if (v.type == DMADESC_KV_FP16) launch_type<DMADESC_KV_FP16>(a, s);
     else launch_type<DMADESC_KV_FP32>(a, s);

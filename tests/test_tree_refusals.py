@@ -91,19 +91,12 @@ def test_keep_and_read_arguments():
 @no_gpu_only
 def test_verify_arguments():
     lib = dd.lib()
-    size = lib.dmadesc_verify_drafts_workspace_bytes
-    need = size(6, 2, 1000)
-    assert need > 0 and need % 256 == 0 and size(6, 2, 100000) > need < size(600, 2, 1000)
-    ok = [P, 1000, P, 1000, 1000, 2, P, P, P, 2, 6, P, P, P, P, P, P, need, NULL]
+    ok = [P, 1000, P, 1000, 1000, 2, P, P, P, 2, 6, P, P, P, P, P, NULL]
     refuses(lib.dmadesc_verify_drafts, ok,
             [(0, NULL), (0, P + 2), (1, -1), (2, P + 1), (3, -8), (4, 0), (4, 1 << 31), (5, 3), (6, NULL),
              (6, P + 2), (7, NULL), (7, P + 1), (8, NULL), (8, P + 2), (9, 1 << 22), (10, 1 << 31), (11, NULL),
-             (11, P + 2), (12, NULL), (12, P + 1), (13, NULL), (13, P + 1), (14, NULL), (14, P + 3), (15, NULL),
-             (16, NULL), (16, P + 16), (17, need - 1)])
+             (11, P + 2), (12, NULL), (12, P + 1), (13, NULL), (13, P + 1), (14, NULL), (14, P + 3), (15, NULL)])
     assert lib.dmadesc_verify_drafts(*[0 if i == 9 else x for i, x in enumerate(ok)]) == 0
-    for bad in ((1 << 31, 2, 1000), (6, 0, 1000), (6, 1 << 22, 1000), (6, 2, 0), (6, 2, 1 << 31),
-                (6, 1 << 20, 1 << 17)):
-        assert size(*bad) == 0, bad
 
 
 def test_binding_refuses_wrong_tensors():

@@ -69,9 +69,9 @@ def attend(pool, table, lens, parents, q, heads_kv, tokens, codes, scale=None):
 
 
 def sound(x):
-    x = np.asarray(x, np.float64)
-    with np.errstate(invalid="ignore"):
-        return np.where((x > 0) & (x < math.inf), x, 0.0)
+    """Negative and NaN as 0, infinity as the largest float32."""
+    x = np.nan_to_num(np.asarray(x, np.float64), nan=0.0, posinf=float(np.finfo(np.float32).max), neginf=0.0)
+    return np.maximum(x, 0.0)
 
 
 def verify(parent, tokens, u, probs, draft=None):
