@@ -833,7 +833,7 @@ int dmadesc_verify_drafts(const void *probs, int64_t probs_stride, const void *d
  *              order, more than DMADESC_TREE_MOST new tokens or more than length, a count
  *              past them or a path that does not ascend in 0 .. n - 1; EPAGE for a new
  *              token on a page outside the pool. A refused request is left as it was
- * rows * kv_heads < 2^25 - 1 (-EINVAL).
+ * rows * kv_heads < 2^23 (-EINVAL).
  */
 int dmadesc_kv_keep(const dmadesc_kv_cache *cache, const int32_t *path, const int32_t *count,
                     const int32_t *q_start, uint64_t total, int32_t *keep, uint8_t *status, void *stream);

@@ -72,8 +72,8 @@ def test_keep_and_read_arguments():
     refuses(lib.dmadesc_kv_keep, ok, [(1, NULL), (1, P + 1), (2, NULL), (2, P + 2), (3, NULL), (3, P + 2),
                                       (4, 1 << 31), (5, NULL), (5, P + 2), (5, P), (6, NULL)])
     assert lib.dmadesc_kv_keep(cache(rows=0, lens=NULL, table=NULL), *ok[1:]) == 0
-    assert lib.dmadesc_kv_keep(cache(rows=(1 << 24) - 1, kv_heads=4), *ok[1:]) == EINVAL      # past a launch
-    assert lib.dmadesc_kv_keep(cache(rows=(1 << 24) - 1, kv_heads=2), *ok[1:]) not in (0, EINVAL)
+    assert lib.dmadesc_kv_keep(cache(rows=1 << 22, kv_heads=2), *ok[1:]) == EINVAL            # past a launch
+    assert lib.dmadesc_kv_keep(cache(rows=(1 << 22) - 1, kv_heads=2), *ok[1:]) not in (0, EINVAL)
     ok = [cache(), P, P, 4, 0, P, 128, 64, P, 128, 64, NULL]
     refuses(lib.dmadesc_kv_read, ok,
             [(1, P + 1), (2, NULL), (2, P + 2), (3, 1 << 31), (4, 3), (5, NULL), (5, P + 8), (6, 4), (6, -8),
