@@ -24,6 +24,8 @@
 // left operand is the page's own V layout (16 tokens of a dimension in 16
 // bytes). Codes go from HBM to registers to the matrix cores; nothing of the
 // cache passes through LDS or is shuffled.
+#include <type_traits>
+
 #include "dd_internal.h"
 #include "dd_kv.hpp"
 
@@ -836,12 +838,15 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     const uint32_t b = __builtin_amdgcn_readfirstlane(it.b);
     const uint32_t head = __builtin_amdgcn_readfirstlane(it.head);
     const uint32_t row0 = __builtin_amdgcn_readfirstlane(it.rt) * kRows;
-    const uint32_t wrow0 = row0 + wv * 32;   // first row of the wave
     const uint32_t s0 = __builtin_amdgcn_readfirstlane(it.s0);
     const int len = __builtin_amdgcn_readfirstlane(it.len), news = __builtin_amdgcn_readfirstlane(it.news);
     const uint32_t nrows = (uint32_t)news * a.group;
     const int per = (int)c.tshift - 4;
     const uint32_t sub_mask = (1u << per) - 1u;
+    // A tree's row tile of 64 rows or fewer: waves 0 and 1 take them over the first half
+    // of every tile, 2 and 3 over the second.
+    const bool pair = kTree && nrows - row0 <= kRows / 2;
+    const uint32_t wrow0 = row0 + (pair ? wv & 1 : wv) * 32;   // first row of the wave
 
     // Least and largest limit of the workgroup's rows, least of the wave's.
     int low = len - 1, high = len - 1, wlow = len - 1;
@@ -1008,26 +1013,30 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
         return;
     }
     // In LDS as tile t begins: its codes; in registers: those of t + 1.
-    for (int t = t0; t < t1; ++t) {
+    auto tile = [&](int t, auto is_pair) {
+        constexpr int kU = decltype(is_pair)::value ? 1 : 2;     // halves of a tile that the wave takes
+        const int half = kU == 1 ? wv >> 1 : 0;     // the first of them
         const int buf = (t - t0) & 1;
         Q8 kf[4];
         f16x8 vf[4];
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 3; ++k) kf[k] = k_operand(buf, k);
+        for (int k = 0; k < 3; ++k) kf[k] = k_operand(buf, k * (2 / kU) + half);
         clean_v(t + 1);
         // The scores, the next codes' conversion under them.
-        f32x16 s[2];
+        f32x16 s[kU];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[0][i] = s[1][i] = 0.0f;
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
         __builtin_amdgcn_sched_barrier(0);
-        constexpr int kSteps = 2 * kK;
+        constexpr int kSteps = kU * kK;
         __builtin_amdgcn_s_setprio(1);              // the matrix unit before the other wave's vector work
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-            if (k + 3 < kSteps) kf[(k + 3) & 3] = k_operand(buf, k + 3);
-            else vf[k + 3 - kSteps] = v_operand(buf, k + 3 - kSteps);
-            s[k & 1] = mfma32(kf[k & 3], qf[k >> 1], s[k & 1]);
+            if (k + 3 < kSteps) kf[(k + 3) & 3] = k_operand(buf, (k + 3) * (2 / kU) + half);
+            else vf[k + 3 - kSteps] = v_operand(buf, k + 3 - kSteps + half * 2 * kX);
+            s[k & (kU - 1)] = mfma32(kf[k & 3], qf[k / kU], s[k & (kU - 1)]);
 #pragma unroll
             for (int m = k * kOps / kSteps; m < (k + 1) * kOps / kSteps; ++m) stage(buf ^ 1, m);
             __builtin_amdgcn_sched_barrier(0);
@@ -1035,22 +1044,24 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
         __builtin_amdgcn_s_setprio(0);
         stage_scales(t + 1, buf ^ 1);
         fetch(t + 2);
-        float ks[4], ve[4], back[4];
+        constexpr int kB = 2 * kU;                  // blocks of 16 tokens
+        float ks[kB], ve[kB], back[kB];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ks[i] = scales[buf][0][i];
-            ve[i] = scales[buf][1][i];
-            back[i] = scales[buf][2][i];
+        for (int i = 0; i < kB; ++i) {
+            ks[i] = scales[buf][0][half * 2 + i];
+            ve[i] = scales[buf][1][half * 2 + i];
+            back[i] = scales[buf][2][half * 2 + i];
             wide |= fabsf(ve[i]) > 40.0f;
         }
         if (t * kTile + kTile - 1 > wlow) {
-            uint32_t sees[4];                           // of a tree: the blocks' tokens, a bit each
+            uint32_t sees[kB];                          // of a tree: the blocks' tokens, a bit each
             if constexpr (kTree)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sees[i] = on ? tree.bits(wv * 32 + col, t * kTile + i * 16 + 8 * h - (len - news)) : 0u;
+                for (int i = 0; i < kB; ++i)
+                    sees[i] = on ? tree.bits((int)(wrow0 - row0) + col,
+                                             t * kTile + (half * 2 + i) * 16 + 8 * h - (len - news)) : 0u;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < kU; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int tok = t * kTile + u * 32 + (i >> 3) * 16 + 8 * h + (i & 7);
@@ -1061,7 +1072,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
         // The reference moves where a row's maximum has risen far enough.
         float tv = -kInf;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kB; ++i) {
             float top = -kInf;
 #pragma unroll
             for (int k = 0; k < 8; ++k) top = fmaxf(top, s[i >> 1][(i & 1) * 8 + k]);
@@ -1081,7 +1092,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
         const float ref = (mx == -kInf ? 0.0f : mx) - kLift;
         if (__builtin_amdgcn_readfirstlane(wide)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kB; ++i) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     l += exp2_(__builtin_fmaf(s[i >> 1][(i & 1) * 8 + k], ks[i], kSum - kLift - ref));
@@ -1102,24 +1113,56 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
         __builtin_amdgcn_s_setprio(1);
         l = __builtin_fmaf(sum, back[0], l);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kB; ++i) {
             sum = 0.0f;
 #pragma unroll
             for (int x = 0; x < kX; ++x) {
                 const int k = i * kX + x;
-                if (k + 3 < 4 * kX) vf[(k + 3) & 3] = v_operand(buf, k + 3);
+                if (k + 3 < kB * kX) vf[(k + 3) & 3] = v_operand(buf, k + 3 + half * 2 * kX);
                 acc[x] = mfma32(vf[k & 3], pf[i & 1], acc[x]);
-                if (i < 3)
+                if (i < kB - 1)
 #pragma unroll
                     for (int e = x * 8 / kX; e < (x + 1) * 8 / kX; ++e) take(i + 1, e);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if (i < 3) l = __builtin_fmaf(sum, back[i + 1], l);
+            if (i < kB - 1) l = __builtin_fmaf(sum, back[i + 1], l);
         }
         __builtin_amdgcn_s_setprio(0);
+    };
+
+    if (kTree && pair) {
+        for (int t = t0; t < t1; ++t) tile(t, std::true_type{});
+    } else {
+        for (int t = t0; t < t1; ++t) tile(t, std::false_type{});
     }
 
     if (a.plan && blockIdx.x == it.base && tid == 0) a.plan[b] = make_uint2(it.base, it.splits);
+    if (kTree && pair) {
+        // Waves 2 and 3 hand what they have to 0 and 1, through the memory of the codes.
+        static_assert(2 * kX * 16 * kWave * 4 <= sizeof kbuf);
+        float *const there = reinterpret_cast<float *>(kbuf) + (wv & 1) * (kX * 16 * kWave) + ln;
+        float *const state = reinterpret_cast<float *>(vbuf) + (wv & 1) * (2 * kWave) + ln;
+        __syncthreads();
+        if (wv >= 2) {
+#pragma unroll
+            for (int x = 0; x < kX; ++x)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) there[(x * 16 + i) * kWave] = acc[x][i];
+            state[0] = mx;
+            state[kWave] = l;
+        }
+        __syncthreads();
+        if (wv >= 2) return;
+        const float mxb = state[0], top = fmaxf(mx, mxb);
+        // In two factors, as the reference moves.
+        const float ha = top == -kInf ? 1.0f : exp2_(0.5f * (mx - top)), hb = top == -kInf ? 1.0f : exp2_(0.5f * (mxb - top));
+        l = l * ha * ha + state[kWave] * hb * hb;
+        mx = top;
+#pragma unroll
+        for (int x = 0; x < kX; ++x)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[x][i] = acc[x][i] * (ha * ha) + there[(x * 16 + i) * kWave] * (hb * hb);
+    }
     l += __shfl_xor(l, 32, kWave);
     if (!on) return;
     const uint64_t orow = (uint64_t)(s0 + jq) * a.heads + hq;
@@ -1138,7 +1181,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
                     const int edge0 = len - news > t0 * kTile ? (len - news) / kTile * kTile : t0 * kTile;
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
-                        const bool nan = tree_nan<kD>(tree, c, tab, head, wv * 32 + col, len - news, edge0,
+                        const bool nan = tree_nan<kD>(tree, c, tab, head, (int)(r - row0), len - news, edge0,
                                                       t1 * kTile < len ? t1 * kTile : len, d + k);
                         o[0] = nan && k == 0 ? __builtin_nanf("") : o[0];
                         o[1] = nan && k == 1 ? __builtin_nanf("") : o[1];

@@ -58,9 +58,10 @@ def check_tree(lens, parents, kv, group, tokens, dim, codes, dtype, seed=0, exps
     assert np.nanmax(d, initial=0) <= 1
     assert np.nanmax(dl, initial=0) <= 1
     assert np.array_equal(np.isnan(lse), np.isnan(ref["lse"]))
-    if against_chain:                                   # a chain is kv_attend's causal chunk, bit for bit
+    if against_chain:                                   # a chain is kv_attend's causal chunk: both within the bound
         c = dd.kv_attend(q, *args, *cache, codes=codes, scale=scale)
-        assert torch.equal(c["out"], r["out"]) and torch.equal(c["lse"], r["lse"])
+        assert (np.abs(c["out"].double().cpu().numpy() - out) <= 2 * bound).all()
+        assert (np.abs(c["lse"].double().cpu().numpy() - lse) <= 2 * lse_bound).all()
 
 
 def some_trees(seed, sizes, branch=4):
