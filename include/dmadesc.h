@@ -756,8 +756,8 @@ size_t dmadesc_kv_attend_workspace_bytes(uint64_t total, uint32_t rows, uint32_t
  * dmadesc_kv_attend_tree: dmadesc_kv_attend for trees. Token j of a request with n
  * new tokens sees the t < lens[r] - n cached before them, itself and the tokens on
  * its way up the tree; one at a place before the cache's first (a request with
- * more new tokens than length) is not there. Arguments, results, limits and
- * workspace as dmadesc_kv_attend's, with
+ * more new tokens than length) is not there. Arguments, results and limits as
+ * dmadesc_kv_attend's, workspace dmadesc_kv_attend_tree_workspace_bytes(...), with
  *   parent     i32[total]. A parent that is no earlier token of the request counts as
  *              -1; tokens past the DMADESC_TREE_MOST-th of a request give unspecified
  *              results (memory-safe; dmadesc_kv_tree_check refuses both)
@@ -770,6 +770,9 @@ int dmadesc_kv_attend_tree(const dmadesc_kv_cache *cache, const void *q, int64_t
                            int64_t q_head_stride, const int32_t *q_start, const int32_t *parent,
                            uint64_t total, uint32_t heads, uint32_t type, float scale, void *out,
                            float *lse, void *ws, size_t ws_bytes, void *stream);
+size_t dmadesc_kv_attend_tree_workspace_bytes(uint64_t total, uint32_t rows, uint32_t heads,
+                                              uint32_t kv_heads, uint32_t dim, uint32_t width,
+                                              uint32_t page_tokens);
 int dmadesc_kv_tree_check(const dmadesc_kv_cache *cache, const int32_t *q_start, const int32_t *parent,
                           uint64_t total, uint8_t *status, void *stream);
 

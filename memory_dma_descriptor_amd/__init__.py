@@ -93,6 +93,7 @@ _EXPORTS = {
     "dmadesc_kv_attend_workspace_bytes": ([_U64, _U32, _U32, _U32, _U32, _U32, _U32], _SIZE),
     "dmadesc_kv_attend_tree": ([_P, _P, _I64, _I64, _P, _P, _U64, _U32, _U32, ctypes.c_float,
                                 _P, _P, _P, _SIZE, _P], ctypes.c_int),
+    "dmadesc_kv_attend_tree_workspace_bytes": ([_U64, _U32, _U32, _U32, _U32, _U32, _U32], _SIZE),
     "dmadesc_kv_tree_check": ([_P, _P, _P, _U64, _P, _P], ctypes.c_int),
     "dmadesc_verify_drafts": ([_P, _I64, _P, _I64, _U64, _U32, _P, _P, _P, _U32, _U64, _P, _P, _P,
                                _P, _P, _P], ctypes.c_int),
@@ -687,9 +688,8 @@ def kv_page_bytes(kv_heads: int, page_tokens: int, dim: int) -> int:
 
 
 @functools.lru_cache(maxsize=4096)
-def _kv_attend_bytes(total, rows, heads, kv_heads, dim, width, page_tokens):
-    return int(lib().dmadesc_kv_attend_workspace_bytes(total, rows, heads, kv_heads, dim, width,
-                                                       page_tokens))
+def _kv_attend_bytes(func, *sizes):
+    return int(getattr(lib(), func + "_workspace_bytes")(*sizes))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -797,7 +797,7 @@ def _attend(func, q, q_start, tree, pool, table, lens, kv_heads, page_tokens, co
                    lse=_new((total, heads), torch.float32, dev, stream))
     if ws is None:
         rows, width = table.shape
-        need = _kv_attend_bytes(total, rows, heads, kv_heads, dim, width, page_tokens)
+        need = _kv_attend_bytes(func, total, rows, heads, kv_heads, dim, width, page_tokens)
         ws = _new(need, torch.uint8, dev, stream) if need else None
     ws_bytes = 0 if ws is None else ws.numel()
     lse = out.get("lse")

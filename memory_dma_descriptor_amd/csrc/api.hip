@@ -420,18 +420,17 @@ int dmadesc_kv_append(const dmadesc_kv_cache *cache, const void *k, int64_t k_to
     return launched(dd::launch_kv_append(a, static_cast<hipStream_t>(stream)));
 }
 
-size_t dmadesc_kv_attend_workspace_bytes(uint64_t total, uint32_t rows, uint32_t heads,
-                                         uint32_t kv_heads, uint32_t dim, uint32_t width,
-                                         uint32_t page_tokens)
+namespace {
+
+size_t attend_bytes(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads, uint32_t dim,
+                    uint32_t width, uint32_t page_tokens, bool tree)
 {
     if (!kv_sizes_ok(kv_heads, page_tokens, dim) || heads == 0 || heads % kv_heads) return 0;
     if (total == 0 || total >= (1ull << 31) || total * heads >= (1ull << 31) || rows == 0 ||
         rows >= (1u << 24) || (uint64_t)width * page_tokens >= (1ull << 31))
         return 0;
-    return dd::ws_kv_attend(total, rows, heads, kv_heads, dim, (uint64_t)width * page_tokens);
+    return dd::ws_kv_attend(total, rows, heads, kv_heads, dim, (uint64_t)width * page_tokens, tree);
 }
-
-namespace {
 
 // dmadesc_kv_attend, or with `tree` dmadesc_kv_attend_tree.
 int attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride, int64_t q_head_stride,
@@ -447,10 +446,10 @@ int attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride,
     if (!out || !aligned16(out) || !aligned4(lse)) return -EINVAL;
     if (tree && (!parent || !aligned4(parent))) return -EINVAL;
     const uint64_t tokens = (uint64_t)cache->width * cache->page_tokens;
-    if (!dd::kv_attend_fits(total, cache->rows, heads, cache->kv_heads, cache->dim, tokens))
+    if (!dd::kv_attend_fits(total, cache->rows, heads, cache->kv_heads, cache->dim, tokens, tree))
         return -EINVAL;
     const size_t need = dd::ws_kv_attend(total, cache->rows, heads, cache->kv_heads, cache->dim,
-                                         tokens);
+                                         tokens, tree);
     if (need > 0 && !ws_ok(ws, ws_bytes, need)) return -EINVAL;
     dd::KvAttendArgs a{*cache, q, q_token_stride, q_head_stride, q_start, total, heads, type,
                        (flags & DMADESC_KV_CAUSAL) != 0, scale, out, lse, ws, parent};
@@ -458,6 +457,20 @@ int attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride,
 }
 
 }  // namespace
+
+size_t dmadesc_kv_attend_workspace_bytes(uint64_t total, uint32_t rows, uint32_t heads,
+                                         uint32_t kv_heads, uint32_t dim, uint32_t width,
+                                         uint32_t page_tokens)
+{
+    return attend_bytes(total, rows, heads, kv_heads, dim, width, page_tokens, false);
+}
+
+size_t dmadesc_kv_attend_tree_workspace_bytes(uint64_t total, uint32_t rows, uint32_t heads,
+                                              uint32_t kv_heads, uint32_t dim, uint32_t width,
+                                              uint32_t page_tokens)
+{
+    return attend_bytes(total, rows, heads, kv_heads, dim, width, page_tokens, true);
+}
 
 int dmadesc_kv_attend(const dmadesc_kv_cache *cache, const void *q, int64_t q_token_stride,
                       int64_t q_head_stride, const int32_t *q_start, uint64_t total,

@@ -223,9 +223,9 @@ hipError_t launch_kv_copy(void *pool, uint64_t npages, uint64_t page_bytes, cons
 
 // False: some launch of the call would pass kKvMaxGroups.
 bool kv_attend_fits(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads, uint32_t dim,
-                    uint64_t tokens);
+                    uint64_t tokens, bool tree);
 size_t ws_kv_attend(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads,
-                    uint32_t dim, uint64_t tokens);
+                    uint32_t dim, uint64_t tokens, bool tree);
 size_t ws_kv_reserve(uint64_t npages, uint64_t n);
 size_t ws_kv_compact(uint64_t npages);
 size_t ws_mr_lookup(uint32_t nregions);

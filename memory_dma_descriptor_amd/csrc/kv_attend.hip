@@ -45,6 +45,10 @@ constexpr uint32_t slots_few(int dim, int nt) { return 256u * few_occupancy(dim,
 constexpr uint32_t slots_many(int dim) { return dim == 64 ? 768 : dim == 128 ? 512 : 256; }
 constexpr uint32_t kLongFew = 32, kLongMany = ~0u;      // tiles of a piece past which two rounds run
 constexpr uint32_t kWholeFew = 20, kWholeMany = 4;      // tiles up to which nothing is split
+// A tree's 32 rows cost a tile more: one request of 900 tokens, 32 rows, 17.6 us whole
+// and 10.6 + 4.3 in pieces and the join.
+constexpr uint32_t kWholeTree = 8;
+constexpr uint32_t whole_few(int nt, bool tree) { return tree && nt == 2 ? kWholeTree : kWholeFew; }
 constexpr uint32_t kMaxSplits = 256;
 constexpr uint32_t kRowsMany = 128;         // query rows of a workgroup of the kernel of many
 constexpr uint32_t kMostFew = 64;           // rows up to which a request is the first's, if both run
@@ -444,7 +448,7 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
     __shared__ TreeRows<kTree ? kRows : 1> tree;
 
     Item it;
-    if (!Plan<kRows, kThreads, slots_few(kD, kNt), 4, kWholeFew, kLongFew>::find(a, blockIdx.x, it)) return;
+    if (!Plan<kRows, kThreads, slots_few(kD, kNt), 4, whole_few(kNt, kTree), kLongFew>::find(a, blockIdx.x, it)) return;
     if constexpr (kTree) {
         if (threadIdx.x == 0) tree.nans = 0;
     } else {
@@ -505,7 +509,7 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
     const int t1 = t0 + part < see ? t0 + part : see;
     const int last_block = len > 0 ? (len - 1) / kBlock : 0;
     const int32_t *const tab = c.table + (uint64_t)b * c.width;
-    if (kTree && t1 * kTile - 1 > low) tree.fill(a, s0, (uint32_t)news, row0);
+    const bool nodes = kTree && t1 * kTile - 1 > low;       // the piece has some of the tree
     const int kblk = col >> 2;              // block of the lane's key rows
     int32_t pk = 0, pv = 0;                 // pages of the next tile, per lane
     u32x4 kr[4][kC], vr[kX];
@@ -561,6 +565,7 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
         load_k(t, true);
         load_v(t, true);
         load_pages(t + kWaves < t1 ? t + kWaves : t);
+        if (nodes) tree.fill(a, s0, (uint32_t)news, row0);  // under these loads
         // The loads of the wave's next tile are in flight under the products of this
         // one. They are made in the last round too: were they conditional, the wait
         // for K at the top would have to be one for all loads.
@@ -681,6 +686,8 @@ __global__ __launch_bounds__(kThreads, few_occupancy(kD, kNt)) void k_kv_attend(
             load_pages(later);
             t += kWaves;
         } while (t < t1);
+    } else if (nodes) {
+        tree.fill(a, s0, (uint32_t)news, row0);             // its barriers are all waves'
     }
 
     // Join the waves: common references first, then the sums through LDS, each
@@ -890,7 +897,6 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     // the next 64 are loaded 16 tiles ahead. Tiles past the last are staged too
     // (from addresses inside a page) and not used.
     const int32_t *const tab = c.table + (uint64_t)b * c.width;
-    if (kTree && t1 * kTile - 1 > low) tree.fill(a, s0, (uint32_t)news, row0);
     const int last_block = len > 0 ? (len - 1) / kBlock : 0;
     u32x4 kr[kLoads], vr[kLoads];
     float sc = 0.0f;
@@ -994,6 +1000,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
         ahead = load_pages(t0 + 16);
         load_k(t0);
         load_v(t0);
+        if (kTree && t1 * kTile - 1 > low) tree.fill(a, s0, (uint32_t)news, row0);   // under these loads
         clean_v(t0);
 #pragma unroll
         for (int n = 0; n < kOps; ++n) stage(0, n);
@@ -1312,16 +1319,21 @@ struct Launch {
 };
 
 Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads, uint32_t dim,
-                 uint64_t tokens)
+                 uint64_t tokens, bool tree)
 {
     Launch p{};
     const uint64_t group = heads / kv_heads, all = total * group;
     const uint64_t mean = (total + rows - 1) / rows * group;
     const uint64_t tiles = (tokens + kTile - 1) / kTile;
-    const bool split_few = tiles > kWholeFew, split_many = tiles > kWholeMany;
+    const bool split_many = tiles > kWholeMany;
     const bool few = mean <= 32u, both = few && total > rows && (total - rows) * group > 1024;
     p.most = !few ? 0u : both ? kMostFew : ~0u;
-    p.tile_rows = mean <= 16 ? 16u : 32u;
+    // A tree over a table so narrow that 16 rows a workgroup go through it whole, with
+    // no join, takes them so where all such pieces run at once (one request of 900
+    // tokens, 32 rows: 13.6 us, in pieces of 32 rows and the join 16).
+    const bool narrow = tree && tiles <= kWholeFew && kv_heads * (all / 16 + rows) <= slots_few((int)dim, 1);
+    p.tile_rows = mean <= 16 || narrow ? 16u : 32u;
+    const bool split_few = tiles > whole_few((int)p.tile_rows / 16, tree);
     // Unsplit pieces: a row tile of a key head each; all rows' whole tiles and one
     // more of each request at most.
     const uint64_t few_rows = both && all > rows * (uint64_t)kMostFew ? rows * (uint64_t)kMostFew : all;
@@ -1393,23 +1405,23 @@ void launch_dim(const KvAttendArgs &k, const AttendArgs &few, const AttendArgs &
 }  // namespace
 
 bool kv_attend_fits(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads, uint32_t dim,
-                    uint64_t tokens)
+                    uint64_t tokens, bool tree)
 {
-    return launch_of(total, rows, heads, kv_heads, dim, tokens).fits;
+    return launch_of(total, rows, heads, kv_heads, dim, tokens, tree).fits;
 }
 
 size_t ws_kv_attend(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_heads,
-                    uint32_t dim, uint64_t tokens)
+                    uint32_t dim, uint64_t tokens, bool tree)
 {
     if (total == 0 || rows == 0) return 0;
-    return launch_of(total, rows, heads, kv_heads, dim, tokens).bytes;
+    return launch_of(total, rows, heads, kv_heads, dim, tokens, tree).bytes;
 }
 
 hipError_t launch_kv_attend(const KvAttendArgs &k, hipStream_t s)
 {
     const dmadesc_kv_cache &c = k.cache;
     const Launch p = launch_of(k.total, c.rows, k.heads, c.kv_heads, c.dim,
-                               (uint64_t)c.width * c.page_tokens);
+                               (uint64_t)c.width * c.page_tokens, k.parent != nullptr);
     AttendArgs few{};
     few.c = kv_view(c);
     if (few.c.npages == 0) few.c.width = 0;             // no page: every length is 0

@@ -53,7 +53,11 @@ def test_bad_caches(bad):
 @no_gpu_only
 def test_attend_tree_arguments():
     lib = dd.lib()
-    need = lib.dmadesc_kv_attend_workspace_bytes(4, 2, 4, 2, 64, 128, 32)
+    size = lib.dmadesc_kv_attend_tree_workspace_bytes
+    need = size(4, 2, 4, 2, 64, 128, 32)
+    assert need > 0 and need % 256 == 0 and size(4, 2, 4, 2, 64, 4, 32) == 0
+    for bad in ((0, 2, 4, 2, 64, 4, 32), (4, 0, 4, 2, 64, 4, 32), (4, 2, 3, 2, 64, 4, 32), (4, 2, 4, 2, 80, 4, 32)):
+        assert size(*bad) == 0, bad
     ok = [cache(width=128), P, 256, 64, P, P, 4, 4, 0, 0.0, P, P, P, need, NULL]
     refuses(lib.dmadesc_kv_attend_tree, ok,
             [(0, NULL), (1, NULL), (1, P + 8), (2, 4), (2, -8), (3, 12), (4, NULL), (5, NULL), (5, P + 2),
