@@ -994,7 +994,6 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
         load_v(t);
     };
 
-    bool wide = false;                              // scales too far apart for one exponential
     if (t0 < t1) {
         here = load_pages(t0);
         ahead = load_pages(t0 + 16);
@@ -1020,7 +1019,8 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
         return;
     }
     // In LDS as tile t begins: its codes; in registers: those of t + 1.
-    auto tile = [&](int t, auto is_pair) {
+    // `wide` goes in and out by value: captured, it takes a vector register in the loop.
+    auto tile = [&](int t, bool wide, auto is_pair) {
         constexpr int kU = decltype(is_pair)::value ? 1 : 2;     // halves of a tile that the wave takes
         const int half = kU == 1 ? wv >> 1 : 0;     // the first of them
         const int buf = (t - t0) & 1;
@@ -1135,12 +1135,14 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
             if (i < kB - 1) l = __builtin_fmaf(sum, back[i + 1], l);
         }
         __builtin_amdgcn_s_setprio(0);
+        return wide;
     };
 
+    bool wide = false;                              // scales too far apart for one exponential
     if (kTree && pair) {
-        for (int t = t0; t < t1; ++t) tile(t, std::true_type{});
+        for (int t = t0; t < t1; ++t) wide = tile(t, wide, std::true_type{});
     } else {
-        for (int t = t0; t < t1; ++t) tile(t, std::false_type{});
+        for (int t = t0; t < t1; ++t) wide = tile(t, wide, std::false_type{});
     }
 
     if (a.plan && blockIdx.x == it.base && tid == 0) a.plan[b] = make_uint2(it.base, it.splits);

@@ -102,6 +102,16 @@ def test_attend_split_over_workgroups(codes, kv, group, dim, length, nodes):
     check_tree([length, 300, length - 77], some_trees(1, [nodes, nodes, 1]), kv, group, 64, dim, codes, "bf16")
 
 
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+@pytest.mark.parametrize("nodes,group", [(8, 4), (30, 1)])
+@pytest.mark.parametrize("requests,length,extra", [(1, 640, 0), (1, 900, 0), (1, 1290, 0), (1, 900, 30), (150, 530, 3)])
+def test_attend_by_table_widths(codes, nodes, group, requests, length, extra):
+    """About 32 rows a request: by 16 rows with no join over a narrow table that fits at
+    once, in pieces of 32 rows past 8 tiles otherwise."""
+    lens = [length] + [40 + i % 7 for i in range(requests - 1)]
+    check_tree(lens, some_trees(9, [nodes] * requests), 2, group, 64, 64, codes, "bf16", extra_width=extra)
+
+
 def test_attend_many_requests():
     # More requests than lanes, some without new tokens, some without a cache before them.
     rng = np.random.default_rng(8)
@@ -216,3 +226,27 @@ def test_attend_tree_without_the_log_sum_exp_and_into_a_given_output():
                           out=dict(out=out[1:6]))
     assert "lse" not in r and torch.equal(out[1:6], whole["out"])
     assert (out[0] == 3).all() and (out[6] == 3).all()
+
+
+def test_two_trees_at_once():
+    """Calls with workspaces of their own on two streams, and one on a stream that
+    meanwhile gets other memory."""
+    kv, tokens, dim = 2, 16, 64
+    rng = np.random.default_rng(3)
+    pool = torch.from_numpy(random_pool(rng, 400, kv, tokens, dim, kc.E4M3)).cuda()
+    jobs = []
+    for nodes in (12, 90):
+        table = i32(rng.permutation(400)[:380].reshape(2, 190))
+        q = torch.randn((2 * nodes, 4, dim), device="cuda", dtype=torch.bfloat16)
+        parent = i32(tc.random_tree(rng, nodes) + tc.random_tree(rng, nodes))
+        jobs.append((q, i32([0, nodes, 2 * nodes]), parent, pool, table, i32([3000, 2500]), kv, tokens))
+    want = [dd.kv_attend_tree(*j) for j in jobs]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(20):
+        got = [dd.kv_attend_tree(*j, stream=s, check=False) for j, s in zip(jobs, sides)]
+        junk = [torch.full((1 << 16,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert junk
+    for w, g in zip(want, got):
+        assert torch.equal(w["out"], g["out"]) and torch.equal(w["lse"], g["lse"])
