@@ -894,12 +894,14 @@ def verify_drafts(probs: torch.Tensor, tokens: torch.Tensor, parent: torch.Tenso
     if out is None:
         out = dict(path=_new(total, torch.int32, dev, stream), count=_new(rows, torch.int32, dev, stream),
                    next=_new(rows, torch.int32, dev, stream), status=_new(rows, torch.uint8, dev, stream))
+        to = [t.data_ptr() for t in out.values()]
+    else:
+        to = [_dev(out["path"], torch.int32, "path", total), _dev(out["count"], torch.int32, "count", rows),
+              _dev(out["next"], torch.int32, "next", rows), _dev(out["status"], torch.uint8, "status", rows)]
     rc = lib().dmadesc_verify_drafts(
         *p, *d, vocab, _KV_TYPE[probs.dtype], _dev(tokens, torch.int32, "tokens", total),
         _dev(parent, torch.int32, "parent", total), _dev(q_start, torch.int32, "q_start"), rows, total,
-        _dev(u, torch.float32, "u", total), _dev(out["path"], torch.int32, "path", total),
-        _dev(out["count"], torch.int32, "count", rows), _dev(out["next"], torch.int32, "next", rows),
-        _dev(out["status"], torch.uint8, "status", rows), _stream(dev, stream))
+        _dev(u, torch.float32, "u", total), *to, _stream(dev, stream))
     _check("dmadesc_verify_drafts", rc)
     if check:
         _kv_refused("dmadesc_verify_drafts", out["status"], stream, out)
@@ -956,10 +958,13 @@ def kv_read(first: torch.Tensor | None, start: torch.Tensor, total: int, pool: t
     if out is None:
         if dtype not in _KV_TYPE:
             raise TypeError(f"dtype: {dtype} is not taken")
-        out = {x: _new((total, kv_heads, dim), dtype, dev, stream) for x in "kv"}
-    dtype = out["k"].dtype
-    kp = _kv_rows(out["k"], "k", total, kv_heads, dim, _KV_TYPE)
-    vp = _kv_rows(out["v"], "v", total, kv_heads, dim, (dtype,))
+        size = total, kv_heads, dim
+        out = dict(k=_new(size, dtype, dev, stream), v=_new(size, dtype, dev, stream))
+        kp, vp = ((t.data_ptr(), kv_heads * dim, dim) for t in out.values())
+    else:
+        dtype = out["k"].dtype
+        kp = _kv_rows(out["k"], "k", total, kv_heads, dim, _KV_TYPE)
+        vp = _kv_rows(out["v"], "v", total, kv_heads, dim, (dtype,))
     f = None if first is None else _dev(first, torch.int32, "first", rows)
     s = _dev(start, torch.int32, "start", rows + 1)
     if check:
