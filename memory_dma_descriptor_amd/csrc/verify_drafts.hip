@@ -18,6 +18,12 @@
 // Then the weights of the last node are summed in 64 even parts, four of a wave,
 // and one wave looks for the place where the running sum passes u W: for the
 // part, for the 64th of it, for the weight.
+//
+// Bound: one compute unit's stream over a row, and steps that wait for one another.
+// 64 requests of 6 rows, 131,072 f32 numbers, draft rows: 25 us, 67 MB read, 20 of them
+// in the sums (13 where the rows are in the caches); 24 trees of 32, 50,257 bf16: 38
+// us, 3.5 a pass; one request of 25, 32,000, certain: 6.8. Several workgroups to a row
+// and a second launch took 7 + 64, 29 + 19 and 4 + 12.
 #include <type_traits>
 
 #include "dd_internal.h"
