@@ -162,3 +162,47 @@ def test_two_verifications_at_once():
     for w, g in zip(want, got):
         for name in w:
             assert torch.equal(w[name], g[name]), name
+
+
+def test_pages_past_4_gib():
+    """The same pages low in one pool and past 4 GiB of another: the same results."""
+    kv, tokens, dim, nodes = 2, 128, 128, 90
+    rng = np.random.default_rng(4)
+    low = torch.from_numpy(random_pool(rng, 12, kv, tokens, dim, kc.E4M3)).cuda()
+    size = low.shape[1]
+    at = (1 << 32) // size - 5                          # some pages before the border, most behind it
+    high = torch.empty((at + 12, size), dtype=torch.uint8, device="cuda")
+    high[at:] = low
+    table = rng.permutation(12)[:10].reshape(2, 5).astype(np.int32)
+    lens, start = i32([600, 580]), i32([0, nodes, nodes + 7])
+    parent = i32(tc.random_tree(rng, nodes) + tc.random_tree(rng, 7))
+    q = torch.randn((nodes + 7, 4, dim), device="cuda").bfloat16()
+    path = torch.full((nodes + 7,), -1, dtype=torch.int32, device="cuda")
+    path[:30] = i32(np.sort(rng.permutation(nodes)[:30]))
+    path[nodes:nodes + 2] = i32([0, 6])
+    def step(pool, table):
+        o = dd.kv_attend_tree(q, start, parent, pool, i32(table), lens, kv, tokens)
+        few = dd.kv_attend_tree(q[nodes:], i32([0, 0, 7]), parent[nodes:], pool, i32(table), lens, kv, tokens)
+        dd.kv_keep(path, i32([30, 2]), start, pool, i32(table), lens, kv, tokens, dim)
+        got = dd.kv_read(None, i32([0, 600, 1180]), 1180, pool, i32(table), lens, kv, tokens, dim)
+        return o["out"], few["out"], got["k"], got["v"]
+    for a, b in zip(step(low, table), step(high, table + at)):
+        assert torch.equal(a, b)
+    assert torch.equal(low, high[at:])
+
+
+def test_rows_past_32_bits():
+    """Rows of probs and draft more than 2^32 numbers from the first."""
+    vocab, rows = 1000, 5
+    wide = torch.empty((rows, 1 << 30), dtype=torch.bfloat16, device="cuda")[:, 7:7 + vocab]
+    g = torch.Generator(device="cuda").manual_seed(0)
+    p = torch.softmax(torch.randn((rows, vocab), generator=g, device="cuda") * 3, 1).bfloat16()
+    d = torch.softmax(p.float().log() + torch.randn(p.shape, generator=g, device="cuda"), 1).bfloat16()
+    args = (i32([0] + d.float().argmax(1).tolist()[:4]), i32([-1, 0, 1, 2, 3]), i32([0, rows]))
+    for seed in range(6):
+        u = torch.rand(rows, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+        want = dd.verify_drafts(p, *args, u, draft=d)
+        far = dd.verify_drafts(wide.copy_(p), *args, u, draft=d)
+        both = dd.verify_drafts(p, *args, u, draft=wide.copy_(d))
+        for name in want:
+            assert torch.equal(want[name], far[name]) and torch.equal(want[name], both[name]), name
