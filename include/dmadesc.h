@@ -804,6 +804,7 @@ int dmadesc_kv_tree_check(const dmadesc_kv_cache *cache, const int32_t *q_start,
  *              Rows without children are not read from draft unless v ends there
  *   tokens     i32[total] token of each row (row 0's is not looked at)
  *   parent     i32[total]; row 0's is not looked at
+ *   q_start, total   as dmadesc_kv_append
  *   u          f32[total] in [0, 1): of row j > 0 for its test, of row 0 for the draw
  *   vocab      1 .. 2^31 - 1; rows < 2^22 (-EINVAL)
  *   path       i32[total]: accepted rows of each request in order, row 0 first, within
@@ -830,6 +831,7 @@ int dmadesc_verify_drafts(const void *probs, int64_t probs_stride, const void *d
  * tokens' again where the scale grew. Places behind the last kept token keep their
  * codes. The pages written are held by this request alone, as append's are.
  *   path, count  as dmadesc_verify_drafts gives them
+ *   q_start, total   as dmadesc_kv_append, whose new tokens these are
  *   keep       i32[rows]: base + count[r], what dmadesc_kv_free cuts the row to;
  *              lens[r] where the request is refused. Not lens itself (-EINVAL)
  *   status     u8[rows] enum dmadesc_kv_status: EINVAL for a bad length, q_start out of

@@ -820,6 +820,7 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     constexpr int kChunkStride = kTile * 16 + 16;   // 8 dimensions of 64 tokens, and a bank step
     constexpr int kLoads = kTile * kD / 16 / kThreads;   // 16-byte loads of a thread, K and V each
     constexpr int kPieces = kD;                     // 16-byte pieces of a block
+    constexpr bool kPairs = kTree && kD < 256;
     constexpr float kRise = 2.0f, kLift = 13.0f;
     // The sum l stands 2^kSum above its terms relative to M. They may lie as far from M
     // as V scales lie from 1: with scales of 2^-64 to 2^127 and 2^29 tokens l stays
@@ -852,11 +853,13 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     const int per = (int)c.tshift - 4;
     const uint32_t sub_mask = (1u << per) - 1u;
     // A tree's row tile of 64 rows or fewer: waves 0 and 1 take them over the first half
-    // of every tile, 2 and 3 over the second. 32 requests, 16 tokens over 200 to 9,000,
+    // of every tile, 2 and 3 over the second. Not at D = 256, where the second loop spills
+    // (12 requests of 64 tokens, 16 heads on 4, e4m3: 80 us without and 89 with, int8 82
+    // both). 32 requests, 16 tokens over 200 to 9,000,
     // 32 heads on 8, D = 128, e4m3: 85 to 88 us, 306 MB read, HBM's 5.5 TB/s while all
     // pieces run (101 us with two waves idle); 12 requests, 64 tokens over 1,000 to
     // 16,000: 130 us, 600 TFLOP/s, the vector unit busy 46 %.
-    const bool pair = kTree && nrows - row0 <= kRows / 2;
+    const bool pair = kPairs && nrows - row0 <= kRows / 2;
     const uint32_t wrow0 = row0 + (pair ? wv & 1 : wv) * 32;   // first row of the wave
 
     // Least and largest limit of the workgroup's rows, least of the wave's.
@@ -1143,14 +1146,14 @@ __global__ __launch_bounds__(kThreads, kD <= 64 ? 3 : kD <= 128 ? 2 : 1) void k_
     };
 
     bool wide = false;                              // scales too far apart for one exponential
-    if (kTree && pair) {
+    if (kPairs && pair) {
         for (int t = t0; t < t1; ++t) wide = tile(t, wide, std::true_type{});
     } else {
         for (int t = t0; t < t1; ++t) wide = tile(t, wide, std::false_type{});
     }
 
     if (a.plan && blockIdx.x == it.base && tid == 0) a.plan[b] = make_uint2(it.base, it.splits);
-    if (kTree && pair) {
+    if (kPairs && pair) {
         // Waves 2 and 3 hand what they have to 0 and 1, through the memory of the codes.
         static_assert(2 * kX * 16 * kWave * 4 <= sizeof kbuf);
         float *const there = reinterpret_cast<float *>(kbuf) + (wv & 1) * (kX * 16 * kWave) + ln;
@@ -1332,7 +1335,9 @@ Launch launch_of(uint64_t total, uint32_t rows, uint32_t heads, uint32_t kv_head
     const uint64_t mean = (total + rows - 1) / rows * group;
     const uint64_t tiles = (tokens + kTile - 1) / kTile;
     const bool split_many = tiles > kWholeMany;
-    const bool few = mean <= 32u, both = few && total > rows && (total - rows) * group > 1024;
+    // Trees of up to 64 rows at D = 256: 32 requests of 16 tokens over 200 to 6,000, 16
+    // heads on 4, e4m3 90 us and 107 by the second, int8 94 and 110.
+    const bool few = mean <= (tree && dim == 256 ? kMostFew : 32u), both = few && total > rows && (total - rows) * group > 1024;
     p.most = !few ? 0u : both ? kMostFew : ~0u;
     // A tree over a table so narrow that 16 rows a workgroup go through it whole, with
     // no join, takes them so where all such pieces run at once (one request of 900

@@ -72,7 +72,7 @@ def some_trees(seed, sizes, branch=4):
 @pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
 @pytest.mark.parametrize("dim,dtype", [(64, "bf16"), (128, "bf16"), (256, "bf16"), (64, "fp16"),
                                        (128, "fp16"), (256, "fp16")])
-@pytest.mark.parametrize("nodes,group,tokens", [(1, 4, 64), (7, 1, 16), (5, 7, 32), (33, 3, 16), (40, 2, 128)])
+@pytest.mark.parametrize("nodes,group,tokens", [(1, 4, 64), (7, 1, 16), (5, 7, 32), (16, 4, 64), (33, 3, 16), (40, 2, 128)])
 def test_attend_tree(codes, dim, dtype, nodes, group, tokens):
     say(f"tree {codes} {dim} {dtype} nodes {nodes} group {group} tokens {tokens}")
     lens = [nodes, 63 + nodes, 64, 200, 129]
@@ -97,7 +97,8 @@ def test_attend_shapes(shape, nodes, group):
 
 @pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
 @pytest.mark.parametrize("kv,group,dim,length,nodes", [(1, 4, 64, 6000, 9), (1, 1, 128, 3000, 70),
-                                                       (2, 8, 256, 2500, 20), (1, 2, 128, 5000, 12)])
+                                                       (2, 8, 256, 2500, 20), (1, 2, 128, 5000, 12),
+                                                       (2, 4, 256, 3100, 16)])
 def test_attend_split_over_workgroups(codes, kv, group, dim, length, nodes):
     check_tree([length, 300, length - 77], some_trees(1, [nodes, nodes, 1]), kv, group, 64, dim, codes, "bf16")
 
