@@ -60,8 +60,13 @@ struct Refused {
 
 constexpr int kN = 4;                                   // numbers that a thread loads at once
 
-// What is negative or NaN counts as 0, infinity as the largest number.
-__device__ __forceinline__ float sound(float x) { return __builtin_amdgcn_fmed3f(x, 0.0f, 3.402823466e38f); }
+// What is negative or NaN counts as 0, infinity as the largest number. (The median
+// is the least of the three where one is NaN, and 0 of a quiet one; a signalling one,
+// which a minimum hands on, is made quiet first.)
+__device__ __forceinline__ float sound(float x)
+{
+    return __builtin_amdgcn_fmed3f(__builtin_canonicalizef(x), 0.0f, 3.402823466e38f);
+}
 
 template <int kType>
 __device__ __forceinline__ float number(const void *p, int64_t at)

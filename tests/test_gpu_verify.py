@@ -160,6 +160,27 @@ def test_verify_rows_out_of_the_ordinary():
     check([[-1, 0]], np.array([0, 5], np.int32), [.6, 1.0], p, None)
 
 
+@pytest.mark.parametrize("certain", [False, True])
+@pytest.mark.parametrize("dtype,bits,inf", [("fp32", (0x7fc00000, 0x7f800001, 0x7fa00000, 0x7fffffff), 0x7f800000),
+                                            ("bf16", (0x7fc0, 0x7f81, 0x7fbf, 0x7fff), 0x7f80),
+                                            ("fp16", (0x7e00, 0x7c01, 0x7dff, 0x7fff), 0x7c00)])
+def test_verify_every_nan_counts_as_zero(dtype, bits, inf, certain):
+    """Quiet and signalling NaN of both signs, in the target's row and in the draft's, at
+    a drafted token and elsewhere; vocabularies below a load's four numbers and above."""
+    whole = {"fp32": torch.int32, "bf16": torch.int16, "fp16": torch.int16}[dtype]
+    sign = 1 << (31 if dtype == "fp32" else 15)
+    size = 2 * sign
+    for nan in [x | s for x in bits for s in (0, sign)] + [inf | sign]:
+        for vocab, token, at in ((3, 1, 1), (3, 0, 2), (6, 2, 2), (6, 2, 5), (300, 7, 7), (300, 7, 255)):
+            for spoil in ("p",) if certain else ("p", "d", "pd"):
+                p, d = (torch.full((2, vocab), 1 / vocab).to(TYPES[dtype]) for _ in range(2))
+                for name, x in (("p", p), ("d", d)):
+                    if name in spoil:
+                        x.view(whole)[0, at] = nan - size if nan & sign else nan
+                for u in ([.999, .5], [0, 1.0], [.6, 0]):
+                    check([[-1, 0]], np.array([0, token], np.int32), u, p, None if certain else d)
+
+
 def test_verify_refuses():
     p = torch.rand((6, 40), device="cuda")
     u = torch.rand(6, device="cuda")
