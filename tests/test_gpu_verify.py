@@ -181,6 +181,34 @@ def test_verify_every_nan_counts_as_zero(dtype, bits, inf, certain):
                     check([[-1, 0]], np.array([0, token], np.int32), u, p, None if certain else d)
 
 
+@pytest.mark.parametrize("certain", [False, True])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("vocab", [262144, 262145, 300001, 1000003])
+def test_verify_long_rows(vocab, dtype, certain):
+    """Rows past 262,144 numbers: parts of more than 4,096, which the workgroup divides
+    once more."""
+    rng = np.random.default_rng(vocab)
+    parents = [[-1, 0, 0, 1], [-1], [-1, 0]]
+    probs = rows_of(rng, 7, vocab, 2.0, dtype)
+    x = torch.log(probs.double().clamp(min=1e-30)) + torch.from_numpy(rng.standard_normal((7, vocab))) * 0.3
+    draft = torch.softmax(x, 1).to(TYPES[dtype])
+    tokens = drafts(rng, parents, draft.double().numpy(), vocab)
+    for u in (rng.random(7), np.array([.9999, .9, .999, 0, 0, .5, .95])):
+        check(parents, tokens, u, probs, None if certain else draft, strided=vocab % 2 == 1)
+
+
+def test_verify_every_part_of_a_long_row():
+    """Equal weights of 2^-20, whose sums are exact: the place is floor(u vocab)."""
+    for vocab in (262144, 262145, 524289, 1000003):
+        n = 400
+        rng = np.random.default_rng(vocab)
+        u = rng.random(n).astype(np.float32)
+        u[:6] = 0, .5, .25, .75, np.float32(1) - np.float32(2.0 ** -24), 2.0 ** -24
+        p = torch.full((1, vocab), 2.0 ** -20, device="cuda").expand(n, vocab)      # one row for all
+        r = dd.verify_drafts(p, i32([0] * n), i32([-1] * n), i32(np.arange(n + 1)), torch.from_numpy(u).cuda())
+        assert r["next"].tolist() == [int(x) for x in np.floor(u.astype(np.float64) * vocab)]
+
+
 def test_verify_refuses():
     p = torch.rand((6, 40), device="cuda")
     u = torch.rand(6, device="cuda")
