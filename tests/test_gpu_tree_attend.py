@@ -214,6 +214,29 @@ def test_attend_tree_spares_bad_pages():
             assert r["out"].shape == q.shape and width == table.shape[1]
 
 
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+@pytest.mark.parametrize("nodes", [3, 80])
+def test_attend_tree_bad_pages_touch_no_other_request(nodes, codes):
+    """Unchecked, a request with bad pages leaves its neighbours' results and the pool
+    as they are, under both kernels."""
+    kv, tokens, dim = 2, 16, 64
+    rng = np.random.default_rng(nodes)
+    pool = torch.from_numpy(random_pool(rng, 18, kv, tokens, dim, codes)).cuda()
+    before = pool.clone()
+    good = rng.permutation(18).astype(np.int32).reshape(3, 6)
+    lens, start = i32([95, 90, 83]), i32([0, nodes, 2 * nodes, 3 * nodes])
+    q = torch.randn((3 * nodes, 4, dim), device="cuda", dtype=torch.bfloat16)
+    tree = i32(tc.random_tree(rng, nodes) * 3)
+    want = dd.kv_attend_tree(q, start, tree, pool, i32(good), lens, kv, tokens, codes=codes)
+    for bad in (18, -1, 1 << 30, -(1 << 31)):
+        table = good.copy()
+        table[1, 1] = table[1, 5] = bad
+        r = dd.kv_attend_tree(q, start, tree, pool, i32(table), lens, kv, tokens, codes=codes, check=False)
+        for x in ("out", "lse"):
+            assert torch.equal(r[x][:nodes], want[x][:nodes]) and torch.equal(r[x][2 * nodes:], want[x][2 * nodes:])
+        assert torch.equal(pool, before)
+
+
 def test_attend_tree_without_the_log_sum_exp_and_into_a_given_output():
     kv, tokens, dim = 2, 16, 128
     rng = np.random.default_rng(2)
