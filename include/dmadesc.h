@@ -826,9 +826,9 @@ int dmadesc_verify_drafts(const void *probs, int64_t probs_stride, const void *d
  * token base + path[q_start[r] + k] goes to place base + k for k < count[r]; path
  * ascends. Where no token moves, nothing is written. From the first that moves on,
  * the blocks are written as dmadesc_kv_append would write these tokens' cached
- * values (code times scale) there: the least scale that holds them, but no smaller
- * one than that of earlier tokens in the block, codes rounded once, the earlier
- * tokens' again where the scale grew. Places behind the last kept token keep their
+ * values (code times scale, also where that is past f32's range) there: the least
+ * scale that holds them, but no smaller one than that of earlier tokens in the block,
+ * codes rounded once, the earlier tokens' again where the scale grew. Places behind the last kept token keep their
  * codes. The pages written are held by this request alone, as append's are.
  *   path, count  as dmadesc_verify_drafts gives them
  *   q_start, total   as dmadesc_kv_append, whose new tokens these are

@@ -21,16 +21,17 @@ __device__ __forceinline__ float pow2(int e)
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Least e >= kMinExp with amax <= c 2^e (c = 448 = 1.75 * 2^8, 127 = 1.984375 * 2^6),
-// from the bits of amax: no logarithm that could be off by one at a border.
+// Least e >= kMinExp with amax 2^down <= c 2^e (c = 448 = 1.75 * 2^8,
+// 127 = 1.984375 * 2^6), from the bits of amax: no logarithm that could be off by one at
+// a border.
 template <int kCodes>
-__device__ __forceinline__ int block_exp(float amax)
+__device__ __forceinline__ int block_exp(float amax, int down = 0)
 {
     const uint32_t bits = __float_as_uint(amax);
     const int e = (int)(bits >> 23) - 127;          // amax = 1.f * 2^e
     const uint32_t frac = bits & 0x7fffffu;
-    const int r = kCodes == DMADESC_KV_E4M3 ? e - 8 + (frac > 0x600000u)
-                                            : e - 6 + (frac > 0x7e0000u);
+    const int r = down + (kCodes == DMADESC_KV_E4M3 ? e - 8 + (frac > 0x600000u)
+                                                    : e - 6 + (frac > 0x7e0000u));
     return r < kMinExp ? kMinExp : r;
 }
 

@@ -3,9 +3,9 @@
 //
 // Mathematics: token base + path[k] goes to base + k. From the first token that
 // moves on, blocks are written as kv_append would write the tokens' cached values
-// (f32 products of code and scale, exact): the least scale 2^e under which they
-// fit the largest code, but no smaller one than earlier tokens of the block have,
-// and codes rounded once. Places past the last kept token keep their codes.
+// (f32 products of code, scale and 2^-kDown, exact): the least scale 2^e under which
+// they fit the largest code, but no smaller one than earlier tokens of the block
+// have, and codes rounded once. Places past the last kept token keep their codes.
 //
 // Work split: one workgroup to K or V of one head of a request, a wave to 64
 // dimensions of a block of 16 tokens. path[k] >= k, so that a block's tokens come
@@ -36,7 +36,9 @@ struct KeepArgs {
     uint8_t *status;
 };
 
-constexpr float kLargest = 3.402823466e38f;
+// Values are held 2^-kDown times as large: 448 under a scale of 2^127 is past f32's
+// range (kv_append gives f32's largest numbers the code 256 under 2^120).
+constexpr int kDown = 24;
 
 // The nearest codes of values in the codes' range, or e4m3's NaN.
 template <int kCodes>
@@ -128,6 +130,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_kv_keep(KeepArgs a)
             from_at += (uint32_t)((at0 + p) % kBlock) * (is_v ? 1u : a.dim);
             from_scale = *scale_from;
             scale_was = *scale_to;
+            from_scale *= pow2(-kDown);
             if (r != place) from_scale = 0.0f;
         }
         // K: lane ln has dimensions 8 (ln % 8) .. + 7 of the slice, of places ln / 8 and
@@ -163,22 +166,6 @@ __global__ __launch_bounds__(kThreads, 6) void k_kv_keep(KeepArgs a)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(code_value<kCodes>(row[i][j / 4], j & 3) * by[i]));
         }
-        // Values that are infinite in f32 (scales from 2^119 on) do not count for the
-        // scale and become the largest code.
-        const bool far = __ballot(!(m <= kLargest)) != 0;
-        if (far) {
-            m = 0.0f;
-            if (is_v) {
-#pragma unroll
-                for (int r = 0; r < kBlock; ++r) m = fmaxf(m, finite_abs(code_value<kCodes>(w[r], 0) * by[r]));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        m = fmaxf(m, finite_abs(code_value<kCodes>(row[i][j / 4], j & 3) * by[i]));
-            }
-        }
         m = wave_max(m);
         if (ln == 0) tops[wv] = m;
         __builtin_amdgcn_s_waitcnt(0x0f70);             // vmcnt(0): all that the wave reads has arrived
@@ -187,9 +174,10 @@ __global__ __launch_bounds__(kThreads, 6) void k_kv_keep(KeepArgs a)
         __syncthreads();                                // before the next round's tops
         if (!on) continue;
         const int e_was = scale_exp(scale_was);
-        int e = block_exp<kCodes>(m);
+        int e = block_exp<kCodes>(m, kDown);
+        e = e < 127 ? e : 127;                          // (-128 under 2^127 stays that code)
         if (old > 0 && e < e_was) e = e_was;
-        const float up = pow2(-e), again = pow2(e_was - e);
+        const float up = pow2(kDown - e), again = pow2(e_was - e);
         if (is_v) {
             u32x4 o;
 #pragma unroll
@@ -197,7 +185,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_kv_keep(KeepArgs a)
                 float y[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = code_value<kCodes>(w[4 * q + i], 0) * by[4 * q + i] * up;
-                const uint32_t fresh = far ? code_quad<kCodes>(y[0], y[1], y[2], y[3]) : near_quad<kCodes>(y);
+                const uint32_t fresh = near_quad<kCodes>(y);
                 // Earlier codes stand unless the scale grew, those past the end always.
                 const uint32_t stay = first_bytes(old - 4 * q) | ~first_bytes(end - 4 * q);
                 o[q] = (fresh & ~stay) | (held[q] & stay);
@@ -227,7 +215,7 @@ __global__ __launch_bounds__(kThreads, 6) void k_kv_keep(KeepArgs a)
                     float y[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) y[j] = code_value<kCodes>(row[i][q], j) * g * f;
-                    o[q] = far ? code_quad<kCodes>(y[0], y[1], y[2], y[3]) : near_quad<kCodes>(y);
+                    o[q] = near_quad<kCodes>(y);
                 }
                 *at = o;
             }

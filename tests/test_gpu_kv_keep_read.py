@@ -95,6 +95,41 @@ def test_keep_zeros_and_nan_codes():
     check_keep([60], [55], [[30, 31, 32]], 1, 16, 64, kc.E4M3, edit=edit)
 
 
+@pytest.mark.parametrize("codes", [kc.E4M3, kc.INT8])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_keep_values_past_the_range_of_float32(codes, dim):
+    """Scales up to 2^127: code times scale is past float32, and the least scale that
+    holds it is still a number. Among blocks of ordinary scales and earlier tokens."""
+    for seed in range(3):
+        rng = np.random.default_rng(seed)
+        def edit(pool, table):
+            for s in kc.split_page(pool, 2, 32, dim)[2:]:
+                far = rng.random(s.shape) < (0.3, 0.7, 1.0)[seed]
+                s[far] = np.exp2(rng.integers(110, 128, s.shape))[far]
+        news = [40, 60, 100, 9]
+        check_keep([50, 63, 130, 30], news, some_paths(rng, news), 2, 32, dim, codes, seed=seed, edit=edit)
+
+
+@pytest.mark.parametrize("codes", [dd.KV_E4M3, dd.KV_INT8])
+def test_keep_what_append_wrote_of_the_largest_numbers(codes):
+    """float32's largest numbers go to a code whose value is past them (256 x 2^120 in
+    e4m3); moved beside small ones they are what they were."""
+    heads, tokens, dim, n = 1, 16, 64, 40
+    top = float(np.finfo(np.float32).max)
+    k = torch.full((n, heads, dim), 1.0, device="cuda")
+    k[20:] = top
+    k[20:, :, ::2] = -top
+    pool = torch.zeros((3, dd.kv_page_bytes(heads, tokens, dim)), dtype=torch.uint8, device="cuda")
+    table, lens = i32([[2, 0, 1]]), i32([n])
+    dd.kv_append(k, k, i32([0, n]), pool, table, lens, tokens, codes=codes)
+    host = pool.cpu().numpy()
+    want = tc.keep(host, np.array([[2, 0, 1]]), [n], [[0, 1, 25, 39]], [n], heads, dim, tokens, codes)
+    dd.kv_keep(i32([0, 1, 25, 39] + [-1] * 36), i32([4]), i32([0, n]), pool, table, lens, heads, tokens, dim, codes=codes)
+    assert tc.same_codes(pool.cpu().numpy(), want, heads, tokens, dim, codes)
+    r = dd.kv_read(None, i32([0, 4]), 4, pool, table, i32([4]), heads, tokens, dim, codes=codes, dtype=torch.float32)
+    assert (r["k"][2:].abs() > 3e38).all() and (r["v"][2:].abs() > 3e38).all()
+
+
 def test_keep_refuses():
     heads, tokens, dim = 2, 16, 64
     rng = np.random.default_rng(1)
