@@ -833,7 +833,8 @@ int dmadesc_verify_drafts(const void *probs, int64_t probs_stride, const void *d
  *   path, count  as dmadesc_verify_drafts gives them
  *   q_start, total   as dmadesc_kv_append, whose new tokens these are
  *   keep       i32[rows]: base + count[r], what dmadesc_kv_free cuts the row to;
- *              lens[r] where the request is refused. Not lens itself (-EINVAL)
+ *              lens[r] where the request is refused. Not lens, path, count or q_start
+ *              itself (-EINVAL)
  *   status     u8[rows] enum dmadesc_kv_status: EINVAL for a bad length, q_start out of
  *              order, more than DMADESC_TREE_MOST new tokens or more than length, a count
  *              past them or a path that does not ascend in 0 .. n - 1; EPAGE for a new

@@ -507,8 +507,10 @@ int dmadesc_kv_keep(const dmadesc_kv_cache *cache, const int32_t *path, const in
     if (!kv_cache_ok(cache) || total >= (1ull << 31)) return -EINVAL;
     if (cache->rows == 0) return 0;
     if ((total > 0 && (!path || !aligned4(path))) || !count || !aligned4(count) || !q_start ||
-        !aligned4(q_start) || !keep || !aligned4(keep) || keep == cache->lens || !status)
+        !aligned4(q_start) || !keep || !aligned4(keep) || !status)
         return -EINVAL;
+    // One workgroup of a request writes keep while the others still read these.
+    if (keep == cache->lens || keep == count || keep == path || keep == q_start) return -EINVAL;
     if (dd::kv_keep_groups(cache->rows, cache->kv_heads) > dd::kKvMaxGroups) return -EINVAL;
     dd::KvKeepArgs a{*cache, path, count, q_start, total, keep, status};
     return launched(dd::launch_kv_keep(a, static_cast<hipStream_t>(stream)));

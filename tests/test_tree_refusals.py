@@ -93,6 +93,15 @@ def test_keep_and_read_arguments():
 
 
 @no_gpu_only
+def test_keep_writes_over_none_of_its_inputs():
+    lib = dd.lib()
+    at = dict(path=0x10000, count=0x20000, q_start=0x30000)
+    for same in (P, *at.values()):
+        assert lib.dmadesc_kv_keep(cache(), *at.values(), 4, same, P, NULL) == EINVAL
+    assert lib.dmadesc_kv_keep(cache(), *at.values(), 4, 0x40000, P, NULL) not in (0, EINVAL)
+
+
+@no_gpu_only
 def test_verify_arguments():
     lib = dd.lib()
     ok = [P, 1000, P, 1000, 1000, 2, P, P, P, 2, 6, P, P, P, P, P, NULL]
