@@ -139,6 +139,22 @@ def test_attend_nan_codes(nodes, length):
     check_tree([length, 40], some_trees(5, [nodes, 3]), 2, 2, 16, 64, kc.E4M3, "bf16", spoil=spoil)
 
 
+@pytest.mark.parametrize("dim,nodes,group", [(64, 6, 2), (128, 20, 4), (256, 30, 2), (64, 90, 3), (128, 70, 2), (256, 140, 1)])
+@pytest.mark.parametrize("share", [0.002, 0.3])
+def test_attend_many_nan_codes(dim, nodes, group, share):
+    """NaN codes all over a tree's tokens and the tile they begin in: siblings' in one word
+    of four tokens, dimensions 16 apart, a row's own and others'."""
+    def spoil(pool, table, q):
+        v = kc.split_page(pool, 2, 32, dim)[1]
+        rng = np.random.default_rng(nodes)
+        for b, (length, n) in enumerate(((1500, nodes), (nodes + 9, nodes), (77, 5))):
+            for at in range(max(0, length - n - 40), length):
+                bad = rng.random((2, dim)) < share
+                v[table[b, at // 32], :, at % 32 // 16, :, at % 16][bad] = 0xff if at % 2 else 0x7f
+    check_tree([1500, nodes + 9, 77], some_trees(5, [nodes, nodes, 5]), 2, group, 32, dim, kc.E4M3, "bf16",
+               spoil=spoil)
+
+
 @pytest.mark.parametrize("nodes", [5, 100])
 def test_attend_more_tokens_than_length(nodes):
     # What dd.kv_tree_check refuses: tokens before the cache's first are not there.
