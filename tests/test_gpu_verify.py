@@ -197,6 +197,32 @@ def test_verify_long_rows(vocab, dtype, certain):
         check(parents, tokens, u, probs, None if certain else draft, strided=vocab % 2 == 1)
 
 
+@pytest.mark.parametrize("certain", [False, True])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("vocab", [4097, 16384, 50257])
+def test_verify_long_rows_with_numbers_out_of_the_ordinary(vocab, dtype, certain):
+    """Rows among whose probabilities are NaN of both kinds, negative numbers, numbers of 2
+    and more and infinity, in the middle of a wave's share and at the row's end."""
+    whole, snan = {"fp32": (torch.int32, 0x7f800001), "bf16": (torch.int16, 0x7f81), "fp16": (torch.int16, 0x7c01)}[dtype]
+    rng = np.random.default_rng(vocab)
+    parents = [[-1, 0, 0, 1], [-1, 0], [-1], [-1], [-1]]
+    n = sum(len(p) for p in parents)
+    for odd in (None, float("nan"), -0.25, 2.5, -0.0, float("inf"), -float("inf")):       # None: a signalling NaN
+        probs = rows_of(rng, n, vocab, 2.0, dtype)
+        x = torch.log(probs.double().clamp(min=1e-30)) + torch.from_numpy(rng.standard_normal((n, vocab))) * 0.3
+        draft = torch.softmax(x, 1).to(TYPES[dtype])
+        tokens = drafts(rng, parents, draft.double().numpy(), vocab)
+        for rows in (probs,) if certain else (probs, draft):
+            for row in range(n - 1):                                                       # the last row is ordinary
+                at = rng.integers(0, vocab, 3)
+                at[0] = vocab - 1 - row % 2
+                if odd is None:
+                    rows.view(whole)[row, at] = snan
+                else:
+                    rows[row, at] = odd
+        check(parents, tokens, rng.random(n), probs, None if certain else draft, strided=vocab % 2 == 1)
+
+
 def test_verify_every_part_of_a_long_row():
     """Equal weights of 2^-20, whose sums are exact: the place is floor(u vocab)."""
     for vocab in (262144, 262145, 524289, 1000003):
