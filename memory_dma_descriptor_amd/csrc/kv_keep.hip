@@ -15,9 +15,9 @@
 // Bound: latency. A wave waits for the request's sizes, then for path and pages
 // together, then for codes and scales; the kernel's own code is kept short (one
 // for all dimensions), since it is fetched anew in each launch. Six waves a SIMD
-// (72 registers): 64 requests of 16 nodes, 8 heads of 128, 7.5 us; 200 requests of up
-// to 60 kept tokens, 4 heads of 256, 17.7 us (five waves: 7.7 and 18.8; eight spill: 8.3
-// and 19.0). Workgroups of eight waves, more blocks a round: 12.2 and 25.6 before that.
+// (72 registers): 64 requests of 16 nodes, 8 heads of 128, 7.0 us; 200 requests of up
+// to 60 kept tokens, 4 heads of 256, 17.4 us (before values were held smaller: six waves
+// 7.5 and 17.7, five 7.7 and 18.8; eight spill: 8.3 and 19.0). Workgroups of eight waves, more blocks a round: 12.2 and 25.6 before that.
 #include "dd_internal.h"
 #include "dd_kv.hpp"
 #include "dd_kv_codes.hpp"

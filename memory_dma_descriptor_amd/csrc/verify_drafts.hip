@@ -9,8 +9,9 @@
 // u d(x) / Q >= w(x) / W with u < 1), and so w = max(p - c d, 0) for one number c:
 // c = 0 at first, and c + W / Q after a refusal. The rows count as having mass 1
 // before any refusal. Without a draft row the drafts are certain, and the
-// remainder is p without the tokens refused. Everything is f64: the answers are
-// whole numbers, so that what is summed in another order must not change them.
+// remainder is p without the tokens refused. Everything is f64 and summed in one fixed
+// order, so that a call answers the same every time; a sum in another order could answer
+// otherwise only where u stands within the last bits of a border.
 //
 // One workgroup a request, one launch. The walk's tests read two numbers each,
 // gathered for all nodes at once, and a first child's test depends on nothing
@@ -21,9 +22,10 @@
 //
 // Bound: one compute unit's stream over a row, and steps that wait for one another.
 // 64 requests of 6 rows, 131,072 f32 numbers, draft rows: 25 us, 67 MB read, 20 of them
-// in the sums (13 where the rows are in the caches); 24 trees of 32, 50,257 bf16: 38
-// us, 3.5 a pass; one request of 25, 32,000, certain: 6.8. Several workgroups to a row
-// and a second launch took 7 + 64, 29 + 19 and 4 + 12.
+// in the sums (13 where the rows are in the caches); without draft rows 14; 24 trees of
+// 32, 50,257 bf16: 36 us, 6 for each refused child of all requests with another behind
+// it; one request of 25, 32,000, certain: 6.8. Several workgroups to a row for the draw,
+// in a second launch, took 7 + 64, 29 + 19 and 4 + 12.
 #include <type_traits>
 
 #include "dd_internal.h"
