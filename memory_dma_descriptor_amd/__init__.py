@@ -769,9 +769,10 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, pool: tor
     _check("dmadesc_kv_append", rc)
 
 
-def _attend(func, q, q_start, tree, pool, table, lens, kv_heads, page_tokens, codes, causal, scale, out,
+def _attend(tree, q, q_start, parent, pool, table, lens, kv_heads, page_tokens, codes, causal, scale, out,
             ws, stream, check):
-    """kv_attend, or with `tree` (parent,) kv_attend_tree."""
+    """kv_attend, or where `tree` is true kv_attend_tree."""
+    func = "dmadesc_kv_attend_tree" if tree else "dmadesc_kv_attend"
     if scale is not None:
         in_f32 = ctypes.c_float(scale).value
         if in_f32 == 0:
@@ -784,10 +785,10 @@ def _attend(func, q, q_start, tree, pool, table, lens, kv_heads, page_tokens, co
     cache = _kv_cache(pool, table, lens, kv_heads, page_tokens, dim, codes)
     qp = _kv_rows(q, "q", total, heads, dim, (torch.bfloat16, torch.float16))
     qs = _dev(q_start, torch.int32, "q_start", cache.rows + 1)
-    up = tuple(_dev(p, torch.int32, "parent", total) for p in tree)
+    up = _dev(parent, torch.int32, "parent", total) if tree else None
     if check:
         if tree:
-            status = kv_tree_check(q_start, tree[0], pool, table, lens, kv_heads, page_tokens, dim, stream)
+            status = kv_tree_check(q_start, parent, pool, table, lens, kv_heads, page_tokens, dim, stream)
         else:
             status = kv_check(q_start, total, pool, table, lens, kv_heads, page_tokens, dim, False,
                               stream)
@@ -801,12 +802,16 @@ def _attend(func, q, q_start, tree, pool, table, lens, kv_heads, page_tokens, co
         ws = _new(need, torch.uint8, dev, stream) if need else None
     ws_bytes = 0 if ws is None else ws.numel()
     lse = out.get("lse")
-    flags = () if tree else (KV_CAUSAL if causal else 0,)
-    rc = getattr(lib(), func)(
-        ctypes.byref(cache), *qp, qs, *up, total, heads, _KV_TYPE[q.dtype], *flags,
-        0.0 if scale is None else scale, _dev(out["out"], q.dtype, "out", total * heads * dim),
-        None if lse is None else _dev(lse, torch.float32, "lse", total * heads),
-        _dev(ws, torch.uint8, "ws") if ws_bytes else None, ws_bytes, _stream(dev, stream))
+    scale = 0.0 if scale is None else scale
+    to = (_dev(out["out"], q.dtype, "out", total * heads * dim),
+          None if lse is None else _dev(lse, torch.float32, "lse", total * heads),
+          _dev(ws, torch.uint8, "ws") if ws_bytes else None, ws_bytes, _stream(dev, stream))
+    if tree:
+        rc = lib().dmadesc_kv_attend_tree(ctypes.byref(cache), *qp, qs, up, total, heads, _KV_TYPE[q.dtype],
+                                          scale, *to)
+    else:
+        rc = lib().dmadesc_kv_attend(ctypes.byref(cache), *qp, qs, total, heads, _KV_TYPE[q.dtype],
+                                     KV_CAUSAL if causal else 0, scale, *to)
     _check(func, rc)
     return out
 
@@ -820,7 +825,7 @@ def kv_attend(q: torch.Tensor, q_start: torch.Tensor, pool: torch.Tensor, table:
     given without it. scale None means 1 / sqrt(dim). check=True first checks the
     table (kv_check), synchronizes and raises DmadescRefused if a request names a
     bad page or length."""
-    return _attend("dmadesc_kv_attend", q, q_start, (), pool, table, lens, kv_heads, page_tokens, codes,
+    return _attend(False, q, q_start, None, pool, table, lens, kv_heads, page_tokens, codes,
                    causal, scale, out, ws, stream, check)
 
 
@@ -833,7 +838,7 @@ def kv_attend_tree(q: torch.Tensor, q_start: torch.Tensor, parent: torch.Tensor,
     parent i32[total] (rows within the request, each less than its own, -1: none).
     check=True first checks the table and the trees (kv_tree_check), synchronizes
     and raises DmadescRefused."""
-    return _attend("dmadesc_kv_attend_tree", q, q_start, (parent,), pool, table, lens, kv_heads,
+    return _attend(True, q, q_start, parent, pool, table, lens, kv_heads,
                    page_tokens, codes, True, scale, out, ws, stream, check)
 
 
